@@ -138,6 +138,36 @@ int w4a8_quant_act(const void* x_bf16, int T, int K, int8_t* q, float* s, void* 
 int w4a8_route_topk(const void* logits_bf16, int T, int E, int k, int32_t* ids, float* w,
                     void* stream);
 
+/* Routing to experts as larger MoE layers do it (beside w4a8_route_topk, which keeps the
+ * plainest softmax gating): softmax or sigmoid scores, a bias per expert that enters the
+ * choice but not the weights, a choice limited to the best groups of experts, renormalised
+ * weights, a factor.  For token t with logits x:
+ *   s[e]  = exp(x[e]) / sum over all E of exp(x)   or, with W4A8_ROUTE_SIGMOID,
+ *           1 / (1 + exp(-x[e]));
+ *   c[e]  = s[e] + bias[e] (no bias: 0); with neither a bias nor W4A8_ROUTE_GROUP_TOP2,
+ *           c[e] = x[e], whose order the scores follow;
+ *   with n_group > 1: experts [g * E / n_group, (g + 1) * E / n_group) form group g, whose
+ *           score is its largest c or, with W4A8_ROUTE_GROUP_TOP2, the sum of its two largest;
+ *           only experts of the topk_group best groups (ties to the lower group) are eligible;
+ *   ids[t]= the k largest c of the eligible experts, largest first, ties to the lower id;
+ *   w[t][j] = s[ids[t][j]], with W4A8_ROUTE_RENORM divided by their sum, times `scale`.
+ * Scores are compared as 64-bit values, so that ids do not depend on fp32 rounding.
+ * An expert whose logit is -inf or NaN, or whose bias is, is masked: it ranks after every
+ * other one (ties to the lower id), adds nothing to its group's score and, should it fill a
+ * row that has fewer than k others, has weight 0; a row with nothing unmasked has all
+ * weights 0.  Its logit, unless -inf or NaN, still counts in the softmax's sum.  Logits of
+ * +inf count as equal and infinitely larger than the rest.
+ *   logits      : device [T][E] of logits_type, aligned to 16 bytes.
+ *   bias_opt    : device float [E] or NULL.
+ *   ids, w      : device int32 / float [T][k], aligned to 16 bytes.
+ * W4A8_EINVAL: k < 1 or > E, E not a multiple of n_group, topk_group outside 1 .. n_group,
+ * topk_group * (E / n_group) < k, an unknown flag or type, a scale that is not finite.
+ * W4A8_EUNSUPPORTED: E > 1024, k > 32, n_group > 32. */
+enum { W4A8_LOGITS_BF16 = 0, W4A8_LOGITS_F16 = 1, W4A8_LOGITS_F32 = 2 };
+enum { W4A8_ROUTE_SIGMOID = 1, W4A8_ROUTE_RENORM = 2, W4A8_ROUTE_GROUP_TOP2 = 4 };
+int w4a8_route_experts(const void* logits, int logits_type, int T, int E, int k, int flags, const float* bias_opt,
+                       int n_group, int topk_group, float scale, int32_t* ids, float* w, void* stream);
+
 /* Workspace bytes needed by w4a8_moe_forward for this layer shape. */
 size_t w4a8_moe_workspace_bytes(int T, int E, int k, int H, int F);
 

@@ -42,6 +42,8 @@ _SIGS = {
     "w4a8_kv_quant": ([_vp, _c_int, _c_int, _c_int, _vp, _vp, _vp], _c_int),
     "w4a8_kv_dequant": ([_vp, _c_int, _c_int, _c_int, _vp, _vp, _vp], _c_int),
     "w4a8_route_topk": ([_vp, _c_int, _c_int, _c_int, _vp, _vp, _vp], _c_int),
+    "w4a8_route_experts": ([_vp, _c_int, _c_int, _c_int, _c_int, _c_int, _vp, _c_int, _c_int, ctypes.c_float, _vp, _vp,
+                            _vp], _c_int),
     "w4a8_moe_workspace_bytes": ([_c_int] * 5, _c_size),
     "w4a8_moe_host_workspace_bytes": ([_c_int] * 5, _c_size),
     "w4a8_moe_rows_capacity": ([_c_int] * 3, _c_int),
@@ -74,6 +76,17 @@ _SIGS = {
     "w4a8_profile_stop": ([ctypes.POINTER(_c_int), ctypes.POINTER(ctypes.c_float), _c_int], _c_int),
 }
 
+# the W8A8 scheme (include/w8a8.h)
+_SIGS_W8A8 = {
+    "w8a8_packed_bytes": ([_c_int] * 4, _c_size),
+    "w8a8_pack_weights": ([_vp, _c_int, _c_int, _c_int, _c_int, _vp, _c_size, _vp, _vp, _vp], _c_int),
+    "w8a8_gemm_workspace_bytes": ([_c_int] * 3, _c_size),
+    "w8a8_gemm": ([_vp, _vp, _c_int, _vp, _c_int, _c_int, _vp, _vp, _c_int, _vp, _c_size, _vp], _c_int),
+    "w8a8_moe_workspace_bytes": ([_c_int] * 5, _c_size),
+    "w8a8_moe_forward": ([_vp, _vp, _c_int, _c_int, _c_int, _vp, _c_int, _vp, _vp, _c_int, _vp, _vp, _c_size, _vp],
+                         _c_int),
+}
+
 KERNEL_KINDS = ["perm", "act_quant", "gemm_up", "requant", "gemm_down", "combine", "gemm_dense", "route"]
 W4A8_DEBUG_SKIP_FIRST_COPY = 1
 
@@ -91,7 +104,7 @@ def lib() -> ctypes.CDLL:
         if not os.path.exists(LIB_PATH):
             raise W4A8Error(f"{LIB_PATH} is missing: build it with `python -m w4a8_quantized_moe_token_b200.build`")
         L = ctypes.CDLL(LIB_PATH)
-        for name, (args, res) in _SIGS.items():
+        for name, (args, res) in (_SIGS | _SIGS_W8A8).items():
             f = getattr(L, name)
             f.argtypes = args
             f.restype = res
@@ -100,7 +113,13 @@ def lib() -> ctypes.CDLL:
 
 
 def exported_symbols():
+    """Names declared in include/w4a8.h."""
     return list(_SIGS)
+
+
+def exported_symbols_w8a8():
+    """Names declared in include/w8a8.h."""
+    return list(_SIGS_W8A8)
 
 
 def _check(status: int, what: str):
@@ -133,6 +152,17 @@ def _dev(t, dtype, name):
 def _need(cond, msg):
     if not cond:
         raise W4A8Error(msg)
+
+
+def _current_device() -> int:
+    _need(torch.cuda.is_available(), "no CUDA device")
+    return torch.cuda.current_device()
+
+
+def _on(t, dtype, name, dev):
+    """_dev for calls with many tensors: the current device is asked for once."""
+    if not t.is_cuda or t.device.index != dev or t.dtype != dtype:
+        _dev(t, dtype, name)
 
 
 def padded_k(K: int, group: int = 128) -> int:
@@ -206,6 +236,34 @@ def w4a8_route_topk(logits: torch.Tensor, k: int, ids: torch.Tensor, w: torch.Te
     _dev(w, torch.float32, "w")
     T, E = logits.shape
     _check(lib().w4a8_route_topk(_ptr(logits), T, E, k, _ptr(ids), _ptr(w), _stream()), "w4a8_route_topk")
+
+
+W4A8_ROUTE_SIGMOID = 1  # scores by sigmoid instead of softmax
+W4A8_ROUTE_RENORM = 2  # chosen scores divided by their sum
+W4A8_ROUTE_GROUP_TOP2 = 4  # group score: sum of the two largest instead of the largest
+_LOGITS_TYPE = {torch.bfloat16: 0, torch.float16: 1, torch.float32: 2}
+
+
+def w4a8_route_experts(logits: torch.Tensor, k: int, ids: torch.Tensor, w: torch.Tensor, flags: int = 0, bias=None,
+                       n_group: int = 1, topk_group: int = 1, scale: float = 1.0):
+    """Experts and gate weights of every token, see include/w4a8.h.
+
+    logits: bf16, fp16 or float32 [T][E]; ids: int32 [T][k] and w: float32 [T][k] (written);
+    flags: W4A8_ROUTE_* OR-ed; bias: float32 [E] or None."""
+    _need(logits.dtype in _LOGITS_TYPE, f"logits must be bf16, fp16 or float32, got {logits.dtype}")
+    _need(logits.dim() == 2, "logits must be [T][E]")
+    T, E = logits.shape
+    _need(tuple(ids.shape) == (T, k), f"ids must be [T={T}][k={k}], got {tuple(ids.shape)}")
+    _need(tuple(w.shape) == (T, k), f"w must be [T={T}][k={k}], got {tuple(w.shape)}")
+    dev = _current_device()
+    _on(logits, logits.dtype, "logits", dev)
+    _on(ids, torch.int32, "ids", dev)
+    _on(w, torch.float32, "w", dev)
+    if bias is not None:
+        _on(bias, torch.float32, "bias", dev)
+        _need(tuple(bias.shape) == (E,), f"bias must be [E={E}], got {tuple(bias.shape)}")
+    _check(lib().w4a8_route_experts(_ptr(logits), _LOGITS_TYPE[logits.dtype], T, E, k, flags, _ptr(bias), n_group,
+                                    topk_group, scale, _ptr(ids), _ptr(w), _stream()), "w4a8_route_experts")
 
 
 def w4a8_moe_workspace_bytes(T, E, k, H, F) -> int:
@@ -400,6 +458,92 @@ def w4a16_gemm(x, packed, N, K, y, ws):
     _need(packed.numel() >= w4a8_packed_bytes(1, N, K, W4A8_LAYOUT_PLAIN),
           "packed is smaller than the packed weights of an N x K matrix")
     _check(lib().w4a16_gemm(_ptr(x), M, _ptr(packed), N, K, _ptr(y), _ptr(ws), ws.numel(), _stream()), "w4a16_gemm")
+
+
+# ------------------------------------------------------------------------- W8A8
+W8A8_F32, W8A8_BF16, W8A8_F16, W8A8_I32 = range(4)
+_OUT_TYPE = {torch.float32: W8A8_F32, torch.bfloat16: W8A8_BF16, torch.float16: W8A8_F16, torch.int32: W8A8_I32}
+
+
+def w8a8_packed_bytes(E: int, N: int, K: int, layout: int) -> int:
+    return lib().w8a8_packed_bytes(E, N, K, layout)
+
+
+def w8a8_pack_weights(w: torch.Tensor, layout: int, packed: torch.Tensor, codes=None, scale=None):
+    """w: bf16 [E][N][K] or [N][K]; packed: uint8 tensor of w8a8_packed_bytes bytes; optional
+    codes int8 [E][N][Kp] and scale float32 [E][N] (all cuda)."""
+    _dev(w, torch.bfloat16, "w")
+    if w.dim() == 2:
+        w = w.unsqueeze(0)
+    _need(w.dim() == 3, "w must be [E][N][K]")
+    E, N, K = w.shape
+    _dev(packed, torch.uint8, "packed")
+    if codes is not None:
+        _dev(codes, torch.int8, "codes")
+        _need(codes.numel() >= E * N * padded_k(K), "codes is smaller than [E][N][Kp]")
+    if scale is not None:
+        _dev(scale, torch.float32, "scale")
+        _need(scale.numel() >= E * N, "scale is smaller than [E][N]")
+    _check(lib().w8a8_pack_weights(_ptr(w), E, N, K, layout, _ptr(packed), packed.numel(), _ptr(codes), _ptr(scale),
+                                   _stream()), "w8a8_pack_weights")
+
+
+def w8a8_gemm_workspace_bytes(M, N, K) -> int:
+    return lib().w8a8_gemm_workspace_bytes(M, N, K)
+
+
+def w8a8_gemm(qa, sa, packed, N, K, y, ws, bias=None):
+    """qa int8 [M][Kp], sa float32 [M], y [M][N] float32, bf16 or fp16 (or int32: the exact
+    sums, sa may be None), bias float32 [N] or None; weights from w8a8_pack_weights."""
+    dev = _current_device()
+    _need(y.dtype in _OUT_TYPE, f"y must be float32, bf16, fp16 or int32, got {y.dtype}")
+    _on(qa, torch.int8, "qa", dev)
+    _on(y, y.dtype, "y", dev)
+    _on(packed, torch.uint8, "packed", dev)
+    _on(ws, torch.uint8, "ws", dev)
+    _need(qa.dim() == 2 and qa.shape[1] == padded_k(K), f"qa must be [M][{padded_k(K)}] for K = {K}, got {tuple(qa.shape)}")
+    M = qa.shape[0]
+    if sa is not None:
+        _on(sa, torch.float32, "sa", dev)
+        _need(sa.numel() == M, f"sa must have {M} entries, has {sa.numel()}")
+    _need(tuple(y.shape) == (M, N), f"y must be [M={M}][N={N}], got {tuple(y.shape)}")
+    if bias is not None:
+        _on(bias, torch.float32, "bias", dev)
+        _need(tuple(bias.shape) == (N,), f"bias must be [N={N}], got {tuple(bias.shape)}")
+    L = lib()
+    _need(packed.numel() >= L.w8a8_packed_bytes(1, N, K, W4A8_LAYOUT_PLAIN),
+          "packed is smaller than the packed weights of an N x K matrix")
+    _check(L.w8a8_gemm(_ptr(qa), _ptr(sa), M, _ptr(packed), N, K, _ptr(bias), _ptr(y), _OUT_TYPE[y.dtype], _ptr(ws),
+                       ws.numel(), _stream()), "w8a8_gemm")
+
+
+def w8a8_moe_workspace_bytes(T, E, k, H, F) -> int:
+    return lib().w8a8_moe_workspace_bytes(T, E, k, H, F)
+
+
+def w8a8_moe_forward(packed_up, packed_down, E, H, F, x, ids, w, out, ws):
+    """The MoE expert FFN with W8A8 experts: the arguments of w4a8_moe_forward, weights from
+    w8a8_pack_weights, ws sized by w8a8_moe_workspace_bytes."""
+    dev = _current_device()
+    _on(x, torch.bfloat16, "x", dev)
+    _on(ids, torch.int32, "ids", dev)
+    _on(w, torch.float32, "w", dev)
+    _on(out, torch.bfloat16, "out", dev)
+    _on(packed_up, torch.uint8, "packed_up", dev)
+    _on(packed_down, torch.uint8, "packed_down", dev)
+    _on(ws, torch.uint8, "ws", dev)
+    _need(ids.dim() == 2, "ids must be [T][k]")
+    T, k = ids.shape
+    _need(tuple(x.shape) == (T, H), f"x must be [T={T}][H={H}], got {tuple(x.shape)}")
+    _need(tuple(w.shape) == (T, k), f"w must be [T={T}][k={k}], got {tuple(w.shape)}")
+    _need(tuple(out.shape) == (T, H), f"out must be [T={T}][H={H}], got {tuple(out.shape)}")
+    L = lib()
+    _need(packed_up.numel() >= L.w8a8_packed_bytes(E, 2 * F, H, W4A8_LAYOUT_GATEUP),
+          "packed_up is smaller than the packed gate|up weights of this layer")
+    _need(packed_down.numel() >= L.w8a8_packed_bytes(E, H, F, W4A8_LAYOUT_PLAIN),
+          "packed_down is smaller than the packed down weights of this layer")
+    _check(L.w8a8_moe_forward(_ptr(packed_up), _ptr(packed_down), E, H, F, _ptr(x), T, _ptr(ids), _ptr(w), k, _ptr(out),
+                              _ptr(ws), ws.numel(), _stream()), "w8a8_moe_forward")
 
 
 def w4a8_debug_inject(flags: int = 0, wait_limit_cycles: int = 0):

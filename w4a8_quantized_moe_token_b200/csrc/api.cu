@@ -3,6 +3,7 @@
 // entry point are in include/w4a8.h.
 #include <cuda_runtime.h>
 
+#include <cmath>
 #include <mutex>
 #include <vector>
 
@@ -20,20 +21,6 @@ inline size_t align_up(size_t v) { return (v + kAlign - 1) / kAlign * kAlign; }
 
 inline bool aligned(const void* p, size_t a) { return (reinterpret_cast<uintptr_t>(p) % a) == 0; }
 
-int sm_count() {
-    static int counts[64] = {0};
-    static std::mutex mu;
-    int dev = 0;
-    if (cudaGetDevice(&dev) != cudaSuccess || dev < 0 || dev >= 64) return 148;
-    std::lock_guard<std::mutex> lock(mu);
-    if (counts[dev] == 0) {
-        int n = 0;
-        if (cudaDeviceGetAttribute(&n, cudaDevAttrMultiProcessorCount, dev) != cudaSuccess || n <= 0) n = 148;
-        counts[dev] = n;
-    }
-    return counts[dev];
-}
-
 // Row capacity of the expert-grouped layout: every non-empty expert's segment is
 // padded up to a multiple of 16 rows.
 int rows_capacity(int T, int E, int k) {
@@ -43,25 +30,13 @@ int rows_capacity(int T, int E, int k) {
     return (int)(((nslots + pad + kRowPad - 1) / kRowPad) * kRowPad);
 }
 
-// Workspace of w4a8_moe_forward: regions in the order of the enum below.
-enum Region {
-    R_ERR, R_CHIST, R_COUNTS, R_OFFS, R_POFFS, R_MTSTART, R_MTTAB, R_PERM, R_INV, R_ROWSRC,
-    R_ACT1, R_S1, R_H, R_ACT2, R_S2, R_Y2,
-    R_XIN, R_IDSIN, R_WIN, R_OUT, R_LOGITS,  // host-buffer variants only
-    R_COUNT
-};
-
-struct MoeLayout {
-    size_t off[R_COUNT + 1];
-    size_t bytes[R_COUNT];
-    int nslots, nchunk, R, Hp, Fp, G1, G2;
-};
+}  // namespace
 
 // w4a16: the W4A16 layer's workspace, in which ACT1 and ACT2 hold bf16 token rows
 // (act16_offset, 16-row blocks) and the INT8 scales and the fp32 h are absent
 // group: weights per scale of the packed weights (64, 128, 256): the token rows are
 // padded to whole groups
-bool moe_layout(int T, int E, int k, int H, int F, bool host_io, MoeLayout* L, bool w4a16 = false, int group = 128) {
+bool moe_layout(int T, int E, int k, int H, int F, bool host_io, MoeLayout* L, bool w4a16, int group) {
     if (T < 0 || E < 1 || E > kMaxExperts || k < 1 || k > 32 || k > E || H < 1 || F < 1) return false;
     if ((long long)T * k >= (1ll << 31)) return false;
     if (group != 64 && group != 128 && group != 256) return false;
@@ -105,14 +80,16 @@ bool moe_layout(int T, int E, int k, int H, int F, bool host_io, MoeLayout* L, b
     return true;
 }
 
+namespace {
+
 int to_status(cudaError_t e) { return e == cudaSuccess ? W4A8_OK : W4A8_ECUDA; }
 
 thread_local DebugInject g_debug;
 
 // the test hook of w4a8_debug_inject, copied into every GEMM launch
 void apply_debug(GemmArgs& a) {
-    a.wait_limit = g_debug.wait_limit > 0 ? g_debug.wait_limit : kWaitLimitCycles;
-    a.debug = g_debug.flags;
+    a.wait_limit = debug_wait_limit();
+    a.debug = debug_flags();
 }
 
 // Optional per-kernel event timing (w4a8_profile_start / w4a8_profile_stop),
@@ -140,23 +117,38 @@ cudaEvent_t prof_event() {
     return e;
 }
 
-// RAII: records an event pair around the kernels launched in its scope
-struct ProfScope {
-    int kind, nlaunch;
-    cudaStream_t st;
-    cudaEvent_t a = nullptr;
-    ProfScope(int k, int n, cudaStream_t s) : kind(k), nlaunch(n), st(s) {
-        if (g_prof.on && (a = prof_event()) != nullptr) cudaEventRecord(a, st);
+}  // namespace
+
+ProfScope::ProfScope(int k, int n, cudaStream_t s) : kind(k), nlaunch(n), st(s) {
+    if (g_prof.on && (a = prof_event()) != nullptr) cudaEventRecord(a, st);
+}
+ProfScope::~ProfScope() {
+    if (a == nullptr) return;
+    cudaEvent_t b = prof_event();
+    if (b == nullptr) return;
+    cudaEventRecord(b, st);
+    g_prof.recs.push_back({kind, a, b});
+    g_prof.launches[kind] += nlaunch;
+}
+
+long long debug_wait_limit() { return g_debug.wait_limit > 0 ? g_debug.wait_limit : kWaitLimitCycles; }
+uint32_t debug_flags() { return g_debug.flags; }
+
+int sm_count() {
+    static int counts[64] = {0};
+    static std::mutex mu;
+    int dev = 0;
+    if (cudaGetDevice(&dev) != cudaSuccess || dev < 0 || dev >= 64) return 148;
+    std::lock_guard<std::mutex> lock(mu);
+    if (counts[dev] == 0) {
+        int n = 0;
+        if (cudaDeviceGetAttribute(&n, cudaDevAttrMultiProcessorCount, dev) != cudaSuccess || n <= 0) n = 148;
+        counts[dev] = n;
     }
-    ~ProfScope() {
-        if (a == nullptr) return;
-        cudaEvent_t b = prof_event();
-        if (b == nullptr) return;
-        cudaEventRecord(b, st);
-        g_prof.recs.push_back({kind, a, b});
-        g_prof.launches[kind] += nlaunch;
-    }
-};
+    return counts[dev];
+}
+
+namespace {
 
 #define W4A8_TRY(expr)                                  \
     do {                                                \
@@ -470,6 +462,22 @@ W4A8_EXPORT int w4a8_route_topk(const void* logits_bf16, int T, int E, int k, in
     ProfScope prof(W4A8_KERNEL_ROUTE, 1, static_cast<cudaStream_t>(stream));
     return to_status(launch_route_topk(static_cast<const uint16_t*>(logits_bf16), T, E, k, ids, w,
                                        static_cast<cudaStream_t>(stream)));
+}
+
+W4A8_EXPORT int w4a8_route_experts(const void* logits, int logits_type, int T, int E, int k, int flags,
+                                   const float* bias_opt, int n_group, int topk_group, float scale, int32_t* ids, float* w,
+                                   void* stream) {
+    if (T < 0 || E < 1 || k < 1 || k > E || n_group < 1 || E % n_group != 0) return W4A8_EINVAL;
+    if (topk_group < 1 || topk_group > n_group || (long long)topk_group * (E / n_group) < k) return W4A8_EINVAL;
+    if (flags & ~(W4A8_ROUTE_SIGMOID | W4A8_ROUTE_RENORM | W4A8_ROUTE_GROUP_TOP2)) return W4A8_EINVAL;
+    if (logits_type < W4A8_LOGITS_BF16 || logits_type > W4A8_LOGITS_F32 || !std::isfinite(scale)) return W4A8_EINVAL;
+    if (E > kMaxExperts || k > 32 || n_group > 32) return W4A8_EUNSUPPORTED;
+    if (T == 0) return W4A8_OK;
+    if (logits == nullptr || ids == nullptr || w == nullptr) return W4A8_EINVAL;
+    if (!aligned(logits, 16) || !aligned(ids, 16) || !aligned(w, 16) || !aligned(bias_opt, 4)) return W4A8_EALIGN;
+    ProfScope prof(W4A8_KERNEL_ROUTE, 1, static_cast<cudaStream_t>(stream));
+    return to_status(launch_route_experts(logits, logits_type, T, E, k, flags, bias_opt, n_group, topk_group, scale, ids, w,
+                                          static_cast<cudaStream_t>(stream)));
 }
 
 W4A8_EXPORT int w4a8_moe_rows_capacity(int T, int E, int k) { return rows_capacity(T, E, k); }

@@ -561,7 +561,14 @@ __device__ __forceinline__ void load_chunk(const float* row, int len, int k0, Ch
     }
 }
 
-template <int kCache, typename TIn>
+// scale of a row with largest magnitude amax: the correctly rounded quotient amax / 127,
+// or (W8A8) the fp32 product amax * (1 / 127)
+template <bool kW8>
+__device__ __forceinline__ float row_scale(float amax) {
+    return kW8 ? __fmul_rn(amax, kInv127) : __fdiv_rn(amax, 127.0f);
+}
+
+template <int kCache, bool kW8, typename TIn>
 __device__ __forceinline__ void quant_row_cta(const TIn* row, int len, int Kp, int r, int RB,
                                               int8_t* __restrict__ act, float* __restrict__ s) {
     __shared__ float red[4];
@@ -591,7 +598,7 @@ __device__ __forceinline__ void quant_row_cta(const TIn* row, int len, int Kp, i
     if ((t & 31) == 0) red[t >> 5] = amax;
     __syncthreads();
     amax = fmaxf(fmaxf(red[0], red[1]), fmaxf(red[2], red[3]));
-    const float sc = __fdiv_rn(amax, 127.0f);
+    const float sc = row_scale<kW8>(amax);
     const float rinv = __fdiv_rn(1.0f, sc);
     auto emit = [&](int ci, const Chunk16& c) {
         uint32_t out[4] = {0u, 0u, 0u, 0u};
@@ -630,6 +637,7 @@ __device__ __forceinline__ void quant_row_cta(const TIn* row, int len, int Kp, i
 // x rows (bf16) -> INT8 rows in expert-grouped order.  CTA t < T quantises token t
 // once (one read of x) and writes the codes to each of its k grouped rows; CTA T + e
 // writes zero codes and scale 0 into the pad rows of expert e.
+template <bool kW8>
 __global__ void __launch_bounds__(128) act_scatter_kernel(const uint16_t* __restrict__ x, int T, int H, int Kp, int k,
                                                           const int* __restrict__ inv,
                                                           const int* __restrict__ offs,
@@ -676,7 +684,7 @@ __global__ void __launch_bounds__(128) act_scatter_kernel(const uint16_t* __rest
     if ((t & 31) == 0) red[t >> 5] = amax;
     __syncthreads();
     amax = fmaxf(fmaxf(red[0], red[1]), fmaxf(red[2], red[3]));
-    const float sc = __fdiv_rn(amax, 127.0f);
+    const float sc = row_scale<kW8>(amax);
     const float rinv = __fdiv_rn(1.0f, sc);
     auto emit = [&](int ci, const Chunk16& c) {
         uint32_t out[4] = {0u, 0u, 0u, 0u};
@@ -708,14 +716,14 @@ __global__ void __launch_bounds__(128) act_scatter_kernel(const uint16_t* __rest
 
 // h rows (fp32, SwiGLU output of the up GEMM) -> INT8 rows for the down GEMM
 // (kCache chunks of 16 per thread stay in registers: 1 covers F <= 2048)
-template <int kCache>
+template <int kCache, bool kW8>
 __global__ void __launch_bounds__(128) requant_kernel(const uint16_t* __restrict__ h, int ldh, int F, int Kp,
                                                       const int* __restrict__ row_src, const int* __restrict__ poffs,
                                                       int E, int RB, int8_t* __restrict__ act, float* __restrict__ s) {
     grid_dep_wait();  // the previous kernel of the forward has completed
     const int r = blockIdx.x;
     if (r >= __ldg(poffs + E)) return;
-    quant_row_cta<kCache, uint16_t>(row_src[r] < 0 ? nullptr : h + (size_t)r * ldh, F, Kp, r, RB, act, s);
+    quant_row_cta<kCache, kW8, uint16_t>(row_src[r] < 0 ? nullptr : h + (size_t)r * ldh, F, Kp, r, RB, act, s);
 }
 
 // ---------------------------------------------------------------------------
@@ -914,17 +922,18 @@ cudaError_t launch_perm(const int32_t* ids, int nslots, int E, int tile_tokens, 
 }
 
 cudaError_t launch_act_scatter(const uint16_t* x, int T, int H, int Kp, int k, const int* inv, const int* offs,
-                               const int* poffs, int E, int rb, int8_t* act, float* s, cudaStream_t stream) {
+                               const int* poffs, int E, int rb, int8_t* act, float* s, cudaStream_t stream, bool w8) {
     if (T == 0) return cudaSuccess;
-    return launch_pdl(act_scatter_kernel, T + E, 128, 0, stream, x, T, H, Kp, k, inv, offs, poffs, rb, act, s);
+    return launch_pdl(w8 ? act_scatter_kernel<true> : act_scatter_kernel<false>, T + E, 128, 0, stream, x, T, H, Kp, k, inv,
+                      offs, poffs, rb, act, s);
 }
 
 cudaError_t launch_requant(const uint16_t* h, int ldh, int F, int Kp, const int* row_src, const int* poffs, int E,
-                           int rows_cap, int rb, int8_t* act, float* s, cudaStream_t stream) {
+                           int rows_cap, int rb, int8_t* act, float* s, cudaStream_t stream, bool w8) {
     if (rows_cap == 0) return cudaSuccess;
-    if (F <= 128 * 16)
-        return launch_pdl(requant_kernel<1>, rows_cap, 128, 0, stream, h, ldh, F, Kp, row_src, poffs, E, rb, act, s);
-    return launch_pdl(requant_kernel<kRowCache>, rows_cap, 128, 0, stream, h, ldh, F, Kp, row_src, poffs, E, rb, act, s);
+    const auto kernel = F <= 128 * 16 ? (w8 ? requant_kernel<1, true> : requant_kernel<1, false>)
+                                      : (w8 ? requant_kernel<kRowCache, true> : requant_kernel<kRowCache, false>);
+    return launch_pdl(kernel, rows_cap, 128, 0, stream, h, ldh, F, Kp, row_src, poffs, E, rb, act, s);
 }
 
 cudaError_t launch_combine(const float* y2, int H, const int* inv, const float* w, int T, int k, uint16_t* out,

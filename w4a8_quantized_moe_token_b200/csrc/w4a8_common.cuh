@@ -387,6 +387,9 @@ __device__ __forceinline__ uint16_t bf16_bits(float v) { return __bfloat16_as_us
 // ---------------------------------------------------------------------------
 // quantisation arithmetic (IEEE fp32, round half to even, no contraction)
 // ---------------------------------------------------------------------------
+// the W8A8 scheme's scales are max|v| * (1 / 127), the constant and the product in fp32
+constexpr float kInv127 = 1.0f / 127.0f;
+
 // symmetric INT8 of one value with scale s > 0
 __device__ __forceinline__ int quant_i8(float x, float s) {
     float r = rintf(__fdiv_rn(x, s));
