@@ -100,7 +100,9 @@ W4A8_EXPORT int w8a8_gemm(const int8_t* qa, const float* sa, int M, const void* 
     a.wscale = reinterpret_cast<const float*>(static_cast<const uint8_t*>(packed) + kHeaderBytes);
     a.act_scale = out_type == W8A8_I32 ? nullptr : sa;
     a.M = M;
-    a.BN = w8_tile_tokens(M);
+    const W8Plan plan = w8_plan_dense(M, a.NT, sm_count());
+    a.BN = plan.bn;
+    op.cg = plan.cg;
     a.mode = kW8Dense;
     a.out_type = out_type;
     a.out = y;
@@ -157,10 +159,10 @@ W4A8_EXPORT int w8a8_moe_forward(const void* packed_up, const void* packed_down,
     float* s2 = at<float>(ws, L, R_S2);
     uint16_t* h = at<uint16_t>(ws, L, R_H);
     float* y2 = at<float>(ws, L, R_Y2);
-    const int tile = w8_tile_tokens(L.nslots / E);
+    const W8Plan plan = w8_plan_grouped(L.nslots / E);
     {
         ProfScope p(W4A8_KERNEL_PERM, perm_launch_count(L.nslots), st);
-        W8_TRY(launch_perm(ids, L.nslots, E, tile, at<int>(ws, L, R_CHIST), L.nchunk, at<int>(ws, L, R_COUNTS), offs, poffs,
+        W8_TRY(launch_perm(ids, L.nslots, E, plan.bn, at<int>(ws, L, R_CHIST), L.nchunk, at<int>(ws, L, R_COUNTS), offs, poffs,
                            mtstart, at<int4>(ws, L, R_MTTAB), at<int>(ws, L, R_PERM), inv, row_src, err, st));
     }
     {
@@ -175,7 +177,8 @@ W4A8_EXPORT int w8a8_moe_forward(const void* packed_up, const void* packed_down,
     a.act_scale = s1;
     a.mt_tab = at<int4>(ws, L, R_MTTAB);
     a.n_mtiles = mtstart + E;
-    a.BN = tile;
+    a.BN = plan.bn;
+    op.cg = plan.cg;
     a.mode = kW8Up;
     a.out_type = W8A8_BF16;
     a.out = h;

@@ -42,6 +42,7 @@ struct W8Args {
     uint32_t* err;            // device error word
     long long wait_limit;     // clock cycles a bounded wait may last
     uint32_t debug;           // test hook
+    int pairs;                // 16-bit rows may be stored two columns at a time (set by the launcher)
     int box_rows;             // token rows per tensor-map box (set by the launcher)
     int plane_x, plane_y;     // tensor-map coordinates of K plane g: (g * plane_x, row + g * plane_y)
 };
@@ -52,11 +53,19 @@ struct W8Operands {
     int matrices;             // number of weight matrices
     const int8_t* x;          // dense: rows of G * 128 bytes; grouped: tiled rows [G][x_rows][128]
     int x_rows;
+    int cg;                   // CTAs per tile (W8Plan)
 };
 
-// tokens per row tile for a mean number of tokens per expert (or the dense layer's rows);
-// the permutation's row-tile table must be built with the same value
-int w8_tile_tokens(int avg_tokens_per_group);
+// Tile shape: cg CTAs work on cg * 128 channels x up to bn tokens.
+struct W8Plan {
+    int cg, bn;
+};
+
+// ... for a dense layer of M rows and NT weight tiles on num_ctas SMs
+W8Plan w8_plan_dense(int M, int NT, int num_ctas);
+// ... for a grouped layer with this mean number of tokens per expert; the permutation's
+// row-tile table must be built with bn
+W8Plan w8_plan_grouped(int avg_tokens);
 cudaError_t launch_gemm_w8a8(W8Args a, const W8Operands& op, int num_ctas, cudaStream_t stream);
 cudaError_t launch_pack_w8(const uint16_t* w, int E, int N, int K, int layout, uint8_t* packed, int8_t* codes, float* scale,
                            cudaStream_t stream);
