@@ -14,7 +14,7 @@
  *
  * The conventions of w4a8.h hold for every entry point here: caller-owned device memory,
  * caller's workspace and stream, argument errors as a w4a8_status, device errors in the
- * workspace's error word (w4a8_last_device_error), nothing allocated.  Serving only: no
+ * workspace (w8a8_gemm_last_error, and w4a8_last_device_error for the layer), nothing allocated.  Serving only: no
  * backward pass.
  */
 #ifndef W8A8_H
@@ -65,6 +65,10 @@ int w8a8_pack_weights(const void* w_bf16, int E, int N, int K, int layout, void*
 size_t w8a8_gemm_workspace_bytes(int M, int N, int K);
 int w8a8_gemm(const int8_t* qa, const float* sa, int M, const void* packed, int N, int K, const float* bias_opt, void* y,
               int out_type, void* ws, size_t ws_bytes, void* stream);
+
+/* Synchronise `stream`, then return the device error bits of the last w8a8_gemm call on
+ * workspace `ws` (0 = none; bit 0 = a bounded wait timed out). */
+int w8a8_gemm_last_error(const void* ws, void* stream);
 
 /* The MoE expert FFN with W8A8 experts: the arguments, routing, permutation, activation
  * quantisation and combine of w4a8_moe_forward,

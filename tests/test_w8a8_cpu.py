@@ -75,7 +75,7 @@ def test_gemm_refusals(lib):
     assert call(qa=vp((1 << 20) + 8)) == EALIGN and call(packed=vp((1 << 20) + 16)) == EALIGN
     assert call(y=ODD) == EALIGN and call(y=vp((1 << 20) + 1), t=1) == EALIGN and call(bias=ODD) == EALIGN
     assert call(ws=vp((1 << 20) + 16)) == EALIGN
-    assert call(n=16) == ENOSPACE
+    assert call(n=16) == ENOSPACE and lib.w8a8_gemm_last_error(None, None) == EINVAL
     assert call(K=1 << 18) == EUNSUPPORTED
     assert call(M=(1 << 31) - 1, N=1 << 20) == EUNSUPPORTED
 

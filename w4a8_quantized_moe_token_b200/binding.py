@@ -82,6 +82,7 @@ _SIGS_W8A8 = {
     "w8a8_pack_weights": ([_vp, _c_int, _c_int, _c_int, _c_int, _vp, _c_size, _vp, _vp, _vp], _c_int),
     "w8a8_gemm_workspace_bytes": ([_c_int] * 3, _c_size),
     "w8a8_gemm": ([_vp, _vp, _c_int, _vp, _c_int, _c_int, _vp, _vp, _c_int, _vp, _c_size, _vp], _c_int),
+    "w8a8_gemm_last_error": ([_vp, _vp], _c_int),
     "w8a8_moe_workspace_bytes": ([_c_int] * 5, _c_size),
     "w8a8_moe_forward": ([_vp, _vp, _c_int, _c_int, _c_int, _vp, _c_int, _vp, _vp, _c_int, _vp, _vp, _c_size, _vp],
                          _c_int),
@@ -154,15 +155,28 @@ def _need(cond, msg):
         raise W4A8Error(msg)
 
 
-def _current_device() -> int:
-    _need(torch.cuda.is_available(), "no CUDA device")
-    return torch.cuda.current_device()
+# The checks of the calls whose kernels take a few microseconds: one look at the current
+# device and stream per call, plain integers instead of c_void_p objects.
+_current_device = torch._C._cuda_getDevice if hasattr(torch._C, "_cuda_getDevice") else torch.cuda.current_device
 
 
-def _on(t, dtype, name, dev):
-    """_dev for calls with many tensors: the current device is asked for once."""
-    if not t.is_cuda or t.device.index != dev or t.dtype != dtype:
-        _dev(t, dtype, name)
+def _raw_stream(dev: int) -> int:
+    return torch._C._cuda_getCurrentRawStream(dev)
+
+
+def _at(t, dtype, name, dev):
+    """Address of a contiguous tensor of this dtype on device `dev` (the current one)."""
+    if t.dtype is not dtype or t.get_device() != dev or not t.is_contiguous():
+        _dev(t, dtype, name)  # raises what it finds
+        _need(False, f"{name} must be contiguous")
+    return t.data_ptr()
+
+
+def _device_of_call(t, name) -> int:
+    """The current device, for a call whose first tensor is t (not a CUDA tensor: raises)."""
+    if not t.is_cuda:
+        raise W4A8Error(f"{name} must be a CUDA tensor")
+    return _current_device()
 
 
 def padded_k(K: int, group: int = 128) -> int:
@@ -250,20 +264,27 @@ def w4a8_route_experts(logits: torch.Tensor, k: int, ids: torch.Tensor, w: torch
 
     logits: bf16, fp16 or float32 [T][E]; ids: int32 [T][k] and w: float32 [T][k] (written);
     flags: W4A8_ROUTE_* OR-ed; bias: float32 [E] or None."""
-    _need(logits.dtype in _LOGITS_TYPE, f"logits must be bf16, fp16 or float32, got {logits.dtype}")
-    _need(logits.dim() == 2, "logits must be [T][E]")
+    dev = _device_of_call(logits, "logits")
+    dtype = logits.dtype
+    if dtype not in _LOGITS_TYPE:
+        raise W4A8Error(f"logits must be bf16, fp16 or float32, got {dtype}")
+    if logits.dim() != 2:
+        raise W4A8Error("logits must be [T][E]")
     T, E = logits.shape
-    _need(tuple(ids.shape) == (T, k), f"ids must be [T={T}][k={k}], got {tuple(ids.shape)}")
-    _need(tuple(w.shape) == (T, k), f"w must be [T={T}][k={k}], got {tuple(w.shape)}")
-    dev = _current_device()
-    _on(logits, logits.dtype, "logits", dev)
-    _on(ids, torch.int32, "ids", dev)
-    _on(w, torch.float32, "w", dev)
+    if ids.shape != (T, k):
+        raise W4A8Error(f"ids must be [T={T}][k={k}], got {tuple(ids.shape)}")
+    if w.shape != (T, k):
+        raise W4A8Error(f"w must be [T={T}][k={k}], got {tuple(w.shape)}")
+    bias_at = None
     if bias is not None:
-        _on(bias, torch.float32, "bias", dev)
-        _need(tuple(bias.shape) == (E,), f"bias must be [E={E}], got {tuple(bias.shape)}")
-    _check(lib().w4a8_route_experts(_ptr(logits), _LOGITS_TYPE[logits.dtype], T, E, k, flags, _ptr(bias), n_group,
-                                    topk_group, scale, _ptr(ids), _ptr(w), _stream()), "w4a8_route_experts")
+        bias_at = _at(bias, torch.float32, "bias", dev)
+        if bias.shape != (E,):
+            raise W4A8Error(f"bias must be [E={E}], got {tuple(bias.shape)}")
+    st = (_lib or lib()).w4a8_route_experts(
+        _at(logits, dtype, "logits", dev), _LOGITS_TYPE[dtype], T, E, k, flags, bias_at, n_group, topk_group, scale,
+        _at(ids, torch.int32, "ids", dev), _at(w, torch.float32, "w", dev), _raw_stream(dev))
+    if st:
+        _check(st, "w4a8_route_experts")
 
 
 def w4a8_moe_workspace_bytes(T, E, k, H, F) -> int:
@@ -495,26 +516,40 @@ def w8a8_gemm_workspace_bytes(M, N, K) -> int:
 def w8a8_gemm(qa, sa, packed, N, K, y, ws, bias=None):
     """qa int8 [M][Kp], sa float32 [M], y [M][N] float32, bf16 or fp16 (or int32: the exact
     sums, sa may be None), bias float32 [N] or None; weights from w8a8_pack_weights."""
-    dev = _current_device()
-    _need(y.dtype in _OUT_TYPE, f"y must be float32, bf16, fp16 or int32, got {y.dtype}")
-    _on(qa, torch.int8, "qa", dev)
-    _on(y, y.dtype, "y", dev)
-    _on(packed, torch.uint8, "packed", dev)
-    _on(ws, torch.uint8, "ws", dev)
-    _need(qa.dim() == 2 and qa.shape[1] == padded_k(K), f"qa must be [M][{padded_k(K)}] for K = {K}, got {tuple(qa.shape)}")
+    dev = _device_of_call(qa, "qa")
+    dtype = y.dtype
+    if dtype not in _OUT_TYPE:
+        raise W4A8Error(f"y must be float32, bf16, fp16 or int32, got {dtype}")
+    Kp = padded_k(K)
+    if qa.dim() != 2 or qa.shape[1] != Kp:
+        raise W4A8Error(f"qa must be [M][{Kp}] for K = {K}, got {tuple(qa.shape)}")
     M = qa.shape[0]
+    if y.shape != (M, N):
+        raise W4A8Error(f"y must be [M={M}][N={N}], got {tuple(y.shape)}")
+    sa_at = bias_at = None
     if sa is not None:
-        _on(sa, torch.float32, "sa", dev)
-        _need(sa.numel() == M, f"sa must have {M} entries, has {sa.numel()}")
-    _need(tuple(y.shape) == (M, N), f"y must be [M={M}][N={N}], got {tuple(y.shape)}")
+        sa_at = _at(sa, torch.float32, "sa", dev)
+        if sa.numel() != M:
+            raise W4A8Error(f"sa must have {M} entries, has {sa.numel()}")
     if bias is not None:
-        _on(bias, torch.float32, "bias", dev)
-        _need(tuple(bias.shape) == (N,), f"bias must be [N={N}], got {tuple(bias.shape)}")
-    L = lib()
-    _need(packed.numel() >= L.w8a8_packed_bytes(1, N, K, W4A8_LAYOUT_PLAIN),
-          "packed is smaller than the packed weights of an N x K matrix")
-    _check(L.w8a8_gemm(_ptr(qa), _ptr(sa), M, _ptr(packed), N, K, _ptr(bias), _ptr(y), _OUT_TYPE[y.dtype], _ptr(ws),
-                       ws.numel(), _stream()), "w8a8_gemm")
+        bias_at = _at(bias, torch.float32, "bias", dev)
+        if bias.shape != (N,):
+            raise W4A8Error(f"bias must be [N={N}], got {tuple(bias.shape)}")
+    L = _lib or lib()
+    if packed.numel() < L.w8a8_packed_bytes(1, N, K, W4A8_LAYOUT_PLAIN):
+        raise W4A8Error("packed is smaller than the packed weights of an N x K matrix")
+    st = L.w8a8_gemm(_at(qa, torch.int8, "qa", dev), sa_at, M, _at(packed, torch.uint8, "packed", dev), N, K, bias_at,
+                     _at(y, dtype, "y", dev), _OUT_TYPE[dtype], _at(ws, torch.uint8, "ws", dev), ws.numel(), _raw_stream(dev))
+    if st:
+        _check(st, "w8a8_gemm")
+
+
+def w8a8_gemm_last_error(ws) -> int:
+    """Device error word of the last w8a8_gemm call on this workspace (synchronises the stream)."""
+    r = lib().w8a8_gemm_last_error(_ptr(ws), _stream())
+    if r < 0:
+        _check(r, "w8a8_gemm_last_error")
+    return r
 
 
 def w8a8_moe_workspace_bytes(T, E, k, H, F) -> int:
@@ -524,26 +559,27 @@ def w8a8_moe_workspace_bytes(T, E, k, H, F) -> int:
 def w8a8_moe_forward(packed_up, packed_down, E, H, F, x, ids, w, out, ws):
     """The MoE expert FFN with W8A8 experts: the arguments of w4a8_moe_forward, weights from
     w8a8_pack_weights, ws sized by w8a8_moe_workspace_bytes."""
-    dev = _current_device()
-    _on(x, torch.bfloat16, "x", dev)
-    _on(ids, torch.int32, "ids", dev)
-    _on(w, torch.float32, "w", dev)
-    _on(out, torch.bfloat16, "out", dev)
-    _on(packed_up, torch.uint8, "packed_up", dev)
-    _on(packed_down, torch.uint8, "packed_down", dev)
-    _on(ws, torch.uint8, "ws", dev)
-    _need(ids.dim() == 2, "ids must be [T][k]")
+    dev = _device_of_call(x, "x")
+    if ids.dim() != 2:
+        raise W4A8Error("ids must be [T][k]")
     T, k = ids.shape
-    _need(tuple(x.shape) == (T, H), f"x must be [T={T}][H={H}], got {tuple(x.shape)}")
-    _need(tuple(w.shape) == (T, k), f"w must be [T={T}][k={k}], got {tuple(w.shape)}")
-    _need(tuple(out.shape) == (T, H), f"out must be [T={T}][H={H}], got {tuple(out.shape)}")
-    L = lib()
-    _need(packed_up.numel() >= L.w8a8_packed_bytes(E, 2 * F, H, W4A8_LAYOUT_GATEUP),
-          "packed_up is smaller than the packed gate|up weights of this layer")
-    _need(packed_down.numel() >= L.w8a8_packed_bytes(E, H, F, W4A8_LAYOUT_PLAIN),
-          "packed_down is smaller than the packed down weights of this layer")
-    _check(L.w8a8_moe_forward(_ptr(packed_up), _ptr(packed_down), E, H, F, _ptr(x), T, _ptr(ids), _ptr(w), k, _ptr(out),
-                              _ptr(ws), ws.numel(), _stream()), "w8a8_moe_forward")
+    if x.shape != (T, H):
+        raise W4A8Error(f"x must be [T={T}][H={H}], got {tuple(x.shape)}")
+    if w.shape != (T, k):
+        raise W4A8Error(f"w must be [T={T}][k={k}], got {tuple(w.shape)}")
+    if out.shape != (T, H):
+        raise W4A8Error(f"out must be [T={T}][H={H}], got {tuple(out.shape)}")
+    L = _lib or lib()
+    if packed_up.numel() < L.w8a8_packed_bytes(E, 2 * F, H, W4A8_LAYOUT_GATEUP):
+        raise W4A8Error("packed_up is smaller than the packed gate|up weights of this layer")
+    if packed_down.numel() < L.w8a8_packed_bytes(E, H, F, W4A8_LAYOUT_PLAIN):
+        raise W4A8Error("packed_down is smaller than the packed down weights of this layer")
+    st = L.w8a8_moe_forward(
+        _at(packed_up, torch.uint8, "packed_up", dev), _at(packed_down, torch.uint8, "packed_down", dev), E, H, F,
+        _at(x, torch.bfloat16, "x", dev), T, _at(ids, torch.int32, "ids", dev), _at(w, torch.float32, "w", dev), k,
+        _at(out, torch.bfloat16, "out", dev), _at(ws, torch.uint8, "ws", dev), ws.numel(), _raw_stream(dev))
+    if st:
+        _check(st, "w8a8_moe_forward")
 
 
 def w4a8_debug_inject(flags: int = 0, wait_limit_cycles: int = 0):

@@ -35,19 +35,16 @@ namespace w4a8 {
 
 namespace {
 
-constexpr int kW8Stages = 7;
 constexpr int kW8EpiWarps = 8;
 constexpr int kW8ProdWarp = kW8EpiWarps;
 constexpr int kW8MmaWarp = kW8EpiWarps + 1;
 constexpr int kW8Threads = 32 * (kW8EpiWarps + 2);
-constexpr int kW8RowsB = 128;                      // token rows per CTA and stage at most
-constexpr int kW8OffA = 0;                         // 1024-aligned (swizzle atoms)
-constexpr int kW8OffB = kW8OffA + kW8Stages * kW8BlockBytes;
-constexpr int kW8OffBar = kW8OffB + kW8Stages * kW8RowsB * 128;
-constexpr int kW8NumBars = 2 * kW8Stages + 4;      // full, empty, 2 x accumulator full / empty
-constexpr int kW8OffMisc = kW8OffBar + kW8NumBars * 8;
-constexpr int kW8Smem = kW8OffMisc + 16 + 1024;    // + alignment slack
-static_assert(kW8Smem <= 227 * 1024, "shared memory over-subscribed");
+constexpr int kW8MaxStages = 12;
+// shared memory: ns weight blocks, ns token blocks (both 1024-aligned: swizzle atoms), the
+// receive buffer of a K split, barriers (full, empty, 2 x accumulator full / empty, receive)
+constexpr int kW8BarBytes = (2 * kW8MaxStages + 5) * 8 + 16;
+constexpr int kW8SmemMax = 227 * 1024 - 1024;  // without the alignment slack
+inline int w8_smem(int ns, int b_stage, int recv) { return ns * (kW8BlockBytes + b_stage) + recv + kW8BarBytes + 1024; }
 
 // ---- PTX ----
 __device__ __forceinline__ void tma_load_2d(uint32_t dst, const CUtensorMap* map, int x, int y, uint32_t bar) {
@@ -105,6 +102,16 @@ __device__ __forceinline__ uint32_t cluster_rank() {
     asm volatile("mov.u32 %0, %%cluster_ctarank;" : "=r"(r));
     return r;
 }
+__device__ __forceinline__ uint32_t cluster_size() {
+    uint32_t r;
+    asm volatile("mov.u32 %0, %%cluster_nctaid.x;" : "=r"(r));
+    return r;
+}
+__device__ __forceinline__ void cluster_arrive() { asm volatile("barrier.cluster.arrive.release;" ::: "memory"); }
+__device__ __forceinline__ void cluster_wait() { asm volatile("barrier.cluster.wait.acquire;" ::: "memory"); }
+__device__ __forceinline__ void st_cluster(uint32_t cluster_addr, uint32_t v) {
+    asm volatile("st.shared::cluster.u32 [%0], %1;" ::"r"(cluster_addr), "r"(v) : "memory");
+}
 __device__ __forceinline__ void cluster_sync() {
     asm volatile("barrier.cluster.arrive.release.aligned;\n\tbarrier.cluster.wait.acquire.aligned;" ::: "memory");
 }
@@ -154,7 +161,7 @@ __device__ __forceinline__ bool w8_wait(uint32_t bar, uint32_t parity, volatile 
             if (*abort_flag) return false;
             if (clock64() - t0 > limit) {
                 *abort_flag = 1;
-                atomicOr(err, kErrTimeout);
+                if (err != nullptr) atomicOr(err, kErrTimeout);
                 return false;
             }
         }
@@ -207,7 +214,11 @@ __device__ __forceinline__ uint16_t to_bits16(float v, int type) {
     return type == W8A8_F16 ? __half_as_ushort(__float2half_rn(v)) : bf16_bits(v);
 }
 
-template <int CG>
+// kSplit (CG = 1, dense): the CTAs of a cluster share one tile, each taking a part of its K
+// planes.  Every CTA sends the INT32 partials of its peers' tokens into their shared memory
+// and finishes its own share of the tokens: exact sums, so the result does not depend on the
+// split, no workspace and no second launch.
+template <int CG, bool kSplit>
 __global__ void __launch_bounds__(kW8Threads, 1)
     gemm_w8a8_kernel(const __grid_constant__ CUtensorMap map_w, const __grid_constant__ CUtensorMap map_x, const W8Args a) {
     constexpr uint32_t kAccCols = 128 * CG;  // columns of one of the two accumulators
@@ -216,15 +227,17 @@ __global__ void __launch_bounds__(kW8Threads, 1)
     const uint32_t base = (raw_addr + 1023u) & ~1023u;
     uint8_t* smem = smem_raw + (base - raw_addr);
     const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
-    const uint32_t rank = CG == 1 ? 0u : cluster_rank();
-    const uint32_t sA = base + kW8OffA, sB = base + kW8OffB;
-    const uint32_t full = base + kW8OffBar, empty = full + 8 * kW8Stages;
-    const uint32_t dfull = empty + 8 * kW8Stages, dempty = dfull + 16;
-    uint32_t* tmem_slot = reinterpret_cast<uint32_t*>(smem + kW8OffMisc);
-    volatile int* abort_flag = reinterpret_cast<volatile int*>(smem + kW8OffMisc + 4);
+    const uint32_t rank = CG == 1 ? 0u : cluster_rank();  // in the pair
+    const uint32_t part = kSplit ? cluster_rank() : 0u, parts = kSplit ? cluster_size() : 1u;
+    const uint32_t NS = (uint32_t)a.ns;
+    const uint32_t sA = base, sB = sA + NS * kW8BlockBytes, recv = sB + NS * a.b_stage;
+    const uint32_t full = recv + a.recv, empty = full + 8 * kW8MaxStages;
+    const uint32_t dfull = empty + 8 * kW8MaxStages, dempty = dfull + 16, recv_full = dempty + 16;
+    uint32_t* tmem_slot = reinterpret_cast<uint32_t*>(smem + (recv_full + 8 - base));
+    volatile int* abort_flag = reinterpret_cast<volatile int*>(tmem_slot + 1);
 
     if (threadIdx.x == 0) {
-        for (int s = 0; s < kW8Stages; ++s) {
+        for (uint32_t s = 0; s < NS; ++s) {
             mbar_init(full + 8 * s, 1);   // a pair's copies all report to its first CTA
             mbar_init(empty + 8 * s, 1);
         }
@@ -232,6 +245,7 @@ __global__ void __launch_bounds__(kW8Threads, 1)
             mbar_init(dfull + 8 * b, 1);
             mbar_init(dempty + 8 * b, kW8EpiWarps * CG);  // in the first CTA, from both
         }
+        if (kSplit) mbar_init(recv_full, kW8EpiWarps * parts);
         *abort_flag = 0;
         fence_mbar_init();
     }
@@ -239,18 +253,21 @@ __global__ void __launch_bounds__(kW8Threads, 1)
     tc_fence_before();
     __syncthreads();
     if (CG == 2) cluster_sync();
+    if (kSplit) cluster_arrive();  // the epilogue warps wait, before they reach for their peers
     tc_fence_after();
     const uint32_t tmem = *tmem_slot;
 
     grid_dep_wait();  // the previous kernel on the stream has completed
     const int total = ceil_div(a.NT, CG) * (a.mt_tab != nullptr ? __ldg(a.n_mtiles) : ceil_div(a.M, a.BN));
-    const int G = a.G;
-    const int u0 = (int)blockIdx.x / CG, du = (int)gridDim.x / CG;
+    // this CTA's K planes [g0, g1) of a tile; kSplit: one tile per cluster
+    const int g0 = kSplit ? (int)((long long)a.G * part / parts) : 0;
+    const int g1 = kSplit ? (int)((long long)a.G * (part + 1) / parts) : a.G;
+    const int u0 = (int)(blockIdx.x / (CG * parts)), du = (int)(gridDim.x / (CG * parts));
 
     if (warp == kW8ProdWarp) {
         // ---------------- producer ----------------
         if (lane == 0) {
-            uint32_t j = 0;
+            uint32_t j = 0, s = 0, ph = 0;  // step, its stage and the stage's phase
             bool ok = true;
             for (int u = u0; u < total && ok; u += du) {
                 const W8Tile t = w8_tile<CG>(u, a, rank);
@@ -260,10 +277,10 @@ __global__ void __launch_bounds__(kW8Threads, 1)
                 const int boxes = ceil_div(rows, a.box_rows);
                 const uint32_t bytes = (uint32_t)kW8BlockBytes + (uint32_t)(boxes * a.box_rows) * 128u;
                 // (a pair's second tile may lie past the last one: read that one again)
-                const int wrow = (t.e * a.NT + min(t.nt, a.NT - 1)) * G * kTileRows;
-                for (int g = 0; g < G; ++g, ++j) {
-                    const uint32_t s = j % kW8Stages;
-                    if (!w8_wait(empty + 8 * s, ((j / kW8Stages) & 1u) ^ 1u, abort_flag, a.err, a.wait_limit)) { ok = false; break; }
+                const int wrow = (t.e * a.NT + min(t.nt, a.NT - 1)) * a.G * kTileRows;
+                for (int g = g0; g < g1; ++g, ++j) {
+                    if (j > 0 && ++s == NS) { s = 0; ph ^= 1u; }
+                    if (!w8_wait(empty + 8 * s, ph ^ 1u, abort_flag, a.err, a.wait_limit)) { ok = false; break; }
                     // test hook: leave the first step's stage empty, so that its consumers time out
                     if (j == 0 && blockIdx.x == 0 && (a.debug & kDebugSkipFirstCopy)) continue;
                     if (rank == 0) mbar_arrive_expect_tx(full + 8 * s, bytes * CG);
@@ -271,23 +288,23 @@ __global__ void __launch_bounds__(kW8Threads, 1)
                     const auto load = CG == 1 ? tma_load_2d : tma_load_2d_pair;
                     load(sA + s * kW8BlockBytes, &map_w, 0, wrow + g * kTileRows, bar);
                     for (int b = 0; b < boxes; ++b)
-                        load(sB + s * (kW8RowsB * 128) + (uint32_t)(b * a.box_rows) * 128u, &map_x, g * a.plane_x,
+                        load(sB + s * a.b_stage + (uint32_t)(b * a.box_rows) * 128u, &map_x, g * a.plane_x,
                              row0 + b * a.box_rows + g * a.plane_y, bar);
                 }
             }
             // Never leave with a copy or a barrier arrival still on its way into this CTA's
             // shared memory: the stages' copies have landed, and (in a run without a
             // timeout) the MMAs that read them have reported back.
-            const uint32_t first = j > (uint32_t)kW8Stages ? j - kW8Stages : 0u;
+            const uint32_t first = j > NS ? j - NS : 0u;
             for (uint32_t q = first; q < j; ++q) {
-                if (rank == 0) w8_drain(full + 8 * (q % kW8Stages), (q / kW8Stages) & 1u, a.wait_limit);
-                if (ok && !*abort_flag) w8_drain(empty + 8 * (q % kW8Stages), (q / kW8Stages) & 1u, a.wait_limit);
+                if (rank == 0) w8_drain(full + 8 * (q % NS), (q / NS) & 1u, a.wait_limit);
+                if (ok && !*abort_flag) w8_drain(empty + 8 * (q % NS), (q / NS) & 1u, a.wait_limit);
             }
         }
         __syncwarp();
     } else if (warp == kW8MmaWarp) {
         // ---------------- MMA issue (the pair's first CTA) ----------------
-        uint32_t j = 0, tile = 0;
+        uint32_t s = 0, ph = 0, tile = 0;
         bool ok = rank == 0;
         for (int u = u0; u < total && ok; u += du, ++tile) {
             const W8Tile t = w8_tile<CG>(u, a, rank);
@@ -296,19 +313,19 @@ __global__ void __launch_bounds__(kW8Threads, 1)
             const uint32_t d = tmem + b * kAccCols;
             if (!w8_wait<CG == 2>(dempty + 8 * b, ((tile >> 1) & 1u) ^ 1u, abort_flag, a.err, a.wait_limit)) break;
             tc_fence_after();
-            for (int g = 0; g < G; ++g, ++j) {
-                const uint32_t s = j % kW8Stages;
-                if (!w8_wait<CG == 2>(full + 8 * s, (j / kW8Stages) & 1u, abort_flag, a.err, a.wait_limit)) { ok = false; break; }
+            for (int g = g0; g < g1; ++g) {
+                if (!w8_wait<CG == 2>(full + 8 * s, ph, abort_flag, a.err, a.wait_limit)) { ok = false; break; }
                 tc_fence_after();
                 if (elect_one()) {
 #pragma unroll
                     for (uint32_t kk = 0; kk < 4; ++kk)
                         mma_i8_ss<CG>(d, smem_desc_sw128(sA + s * kW8BlockBytes + kk * 32),
-                                      smem_desc_sw128(sB + s * (kW8RowsB * 128) + kk * 32), idesc, (g | kk) != 0);
+                                      smem_desc_sw128(sB + s * a.b_stage + kk * 32), idesc, g != g0 || kk != 0);
                     w8_commit<CG>(empty + 8 * s);
-                    if (g == G - 1) w8_commit<CG>(dfull + 8 * b);
+                    if (g == g1 - 1) w8_commit<CG>(dfull + 8 * b);
                 }
                 __syncwarp();
+                if (++s == NS) { s = 0; ph ^= 1u; }
             }
         }
     } else {
@@ -317,6 +334,7 @@ __global__ void __launch_bounds__(kW8Threads, 1)
         const int r = q * 32 + lane;               // tile row = tensor-memory lane
         const int odd = lane & 1;
         uint32_t tile = 0;
+        if (kSplit) cluster_wait();  // every CTA's barriers stand
         for (int u = u0; u < total; u += du, ++tile) {
             const W8Tile t = w8_tile<CG>(u, a, rank);
             const uint32_t b = tile & 1u;
@@ -326,6 +344,57 @@ __global__ void __launch_bounds__(kW8Threads, 1)
             const float bias = (a.bias != nullptr && n < a.nvalid) ? __ldg(a.bias + n) : 0.f;
             if (!w8_wait(dfull + 8 * b, (tile >> 1) & 1u, abort_flag, a.err, a.wait_limit)) break;
             tc_fence_after();
+            if (kSplit) {
+                // tokens [p * per, (p + 1) * per) are finished by CTA p, which keeps the
+                // partials of source s at recv[s][token][channel]
+                const int per = ceil_div(t.nrows, (int)parts);
+                for (int c0 = half * 32; c0 < t.nrows; c0 += 64) {
+                    uint32_t v[32];
+                    tmem_ld32(tmem + ((uint32_t)(q * 32) << 16) + (uint32_t)c0, v);
+                    tmem_ld_wait();
+                    int p = c0 / per, left = (p + 1) * per - c0;  // tokens left for CTA p
+                    uint32_t dst = mapa(recv, (uint32_t)p) + (uint32_t)(((int)part * per + c0 - p * per) * kTileRows + r) * 4u;
+#pragma unroll
+                    for (int i = 0; i < 32; ++i) {
+                        if (c0 + i < t.nrows) {
+                            if (left == 0) {
+                                ++p;
+                                left = per;
+                                dst = mapa(recv, (uint32_t)p) + (uint32_t)((int)part * per * kTileRows + r) * 4u;
+                            }
+                            st_cluster(dst, v[i]);
+                            dst += kTileRows * 4;
+                            --left;
+                        }
+                    }
+                }
+                __syncwarp();
+                if (lane < (int)parts) {
+                    asm volatile("fence.acq_rel.cluster;" ::: "memory");
+                    mbar_arrive_cluster(mapa(recv_full, (uint32_t)lane));
+                }
+                __syncwarp();
+                if (!w8_wait<true>(recv_full, 0, abort_flag, a.err, a.wait_limit)) break;
+                const int first = (int)part * per, count = min(per, t.nrows - first);
+                const int32_t* rb = reinterpret_cast<const int32_t*>(smem + (recv - base)) + r;
+                for (int i = half; i < count; i += 2) {
+                    int sum = 0;
+                    for (uint32_t src = 0; src < parts; ++src) sum += rb[((int)src * per + i) * kTileRows];
+                    const size_t at = (size_t)(t.row0 + first + i) * a.ldo + n;
+                    if (n < a.nvalid) {
+                        if (a.out_type == W8A8_I32) {
+                            static_cast<int32_t*>(a.out)[at] = sum;
+                        } else {
+                            const float y = __int2float_rn(sum) * (sw * __ldg(a.act_scale + t.row0 + first + i)) + bias;
+                            if (a.out_type == W8A8_F32)
+                                static_cast<float*>(a.out)[at] = y;
+                            else
+                                static_cast<uint16_t*>(a.out)[at] = to_bits16(y, a.out_type);
+                        }
+                    }
+                }
+                break;
+            }
             for (int c0 = half * 32; c0 < t.nrows; c0 += 64) {
                 const int ncol = min(32, t.nrows - c0);  // tokens of this chunk
                 const float sa = lane < ncol && a.act_scale != nullptr ? __ldg(a.act_scale + t.row0 + c0 + lane) : 0.f;
@@ -393,7 +462,8 @@ __global__ void __launch_bounds__(kW8Threads, 1)
     }
 
     __syncthreads();
-    if (CG == 2) {
+    if (kSplit && warp >= kW8ProdWarp) cluster_wait();  // (the epilogue warps have waited)
+    if (CG == 2 || kSplit) {
         // after a timeout the pair's copies and arrivals are not accounted for: give them
         // ample time (50 us) to land before either CTA's shared memory goes away
         if (*abort_flag) {
@@ -402,6 +472,12 @@ __global__ void __launch_bounds__(kW8Threads, 1)
             }
         }
         cluster_sync();
+    }
+    if (a.status != nullptr) {
+        // one word per CTA, every word written by every launch: nothing to clear beforehand
+        if (threadIdx.x == 0) a.status[blockIdx.x] = *abort_flag ? kErrTimeout : 0u;
+        if (blockIdx.x == 0)
+            for (int i = (int)gridDim.x + (int)threadIdx.x; i < kW8StatusWords; i += kW8Threads) a.status[i] = 0u;
     }
     if (warp == kW8MmaWarp) {
         tc_fence_after();
@@ -531,9 +607,10 @@ cudaError_t make_map(CUtensorMap* m, const void* base, uint64_t width, uint64_t 
 
 namespace {
 
-template <int CG>
-cudaError_t launch_instance(const CUtensorMap& mw, const CUtensorMap& mx, const W8Args& a, int num_ctas, cudaStream_t stream) {
-    const auto kernel = gemm_w8a8_kernel<CG>;
+template <int CG, bool kSplit>
+cudaError_t launch_instance(const CUtensorMap& mw, const CUtensorMap& mx, const W8Args& a, int smem, int grid, int cluster,
+                            cudaStream_t stream) {
+    const auto kernel = gemm_w8a8_kernel<CG, kSplit>;
     static std::mutex mu;
     static int clusters[64] = {0};  // per device: pairs that fit at once (CG = 2), 1 once prepared
     int dev = 0;
@@ -541,26 +618,27 @@ cudaError_t launch_instance(const CUtensorMap& mw, const CUtensorMap& mx, const 
     if (e != cudaSuccess) return e;
     if (dev < 0 || dev >= 64) return cudaErrorInvalidDevice;
     cudaLaunchConfig_t cfg = {};
-    cfg.gridDim = num_ctas / CG * CG;
+    cfg.gridDim = grid;
     cfg.blockDim = kW8Threads;
-    cfg.dynamicSmemBytes = kW8Smem;
+    cfg.dynamicSmemBytes = smem;
     cfg.stream = stream;
     cudaLaunchAttribute attr[2];
     attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
     attr[0].val.programmaticStreamSerializationAllowed = 1;
     attr[1].id = cudaLaunchAttributeClusterDimension;
-    attr[1].val.clusterDim.x = CG;
+    attr[1].val.clusterDim.x = (unsigned)cluster;
     attr[1].val.clusterDim.y = attr[1].val.clusterDim.z = 1;
     cfg.attrs = attr;
-    cfg.numAttrs = CG == 1 ? 1 : 2;
+    cfg.numAttrs = cluster == 1 ? 1 : 2;
     {
         std::lock_guard<std::mutex> lock(mu);
         if (clusters[dev] == 0) {
-            e = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, kW8Smem);
+            e = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, 227 * 1024);
             if (e != cudaSuccess) return e;
             int n = 1;
             if (CG == 2) {
                 cudaLaunchConfig_t q = cfg;
+                q.dynamicSmemBytes = 227 * 1024;
                 q.attrs = attr + 1;
                 q.numAttrs = 1;
                 e = cudaOccupancyMaxActiveClusters(&n, kernel, &q);
@@ -569,7 +647,7 @@ cudaError_t launch_instance(const CUtensorMap& mw, const CUtensorMap& mx, const 
             }
             clusters[dev] = n;
         }
-        if (CG == 2 && (int)cfg.gridDim.x > clusters[dev] * CG) cfg.gridDim = clusters[dev] * CG;
+        if (CG == 2 && grid > clusters[dev] * CG) cfg.gridDim = clusters[dev] * CG;
     }
     return cudaLaunchKernelEx(&cfg, kernel, mw, mx, a);
 }
@@ -577,32 +655,46 @@ cudaError_t launch_instance(const CUtensorMap& mw, const CUtensorMap& mx, const 
 }  // namespace
 
 W8Plan w8_plan_grouped(int avg_tokens) {
-    if (avg_tokens < 64) return {1, 128};
+    if (avg_tokens < 64) return {1, 128, 1};
     const int want = avg_tokens + avg_tokens / 10;  // most experts' rows in equal tiles
     const int tiles = ceil_div(want, 256);
-    return {2, round_up(ceil_div(want, tiles), 32)};
+    return {2, round_up(ceil_div(want, tiles), 32), 1};
 }
 
-W8Plan w8_plan_dense(int M, int NT, int num_ctas) {
-    if (M <= 128) return {1, round_up(M, 16)};
-    W8Plan best = {2, 256};
-    long long best_cost = 0;
-    for (int bn = 256; bn >= 64; bn -= 32) {
-        const long long tiles = (long long)ceil_div(M, bn) * ceil_div(NT, 2);
-        const long long cost = (tiles + num_ctas / 2 - 1) / (num_ctas / 2) * (bn + 64);
-        if (best_cost == 0 || cost < best_cost) {
+// The cheapest of the tile shapes by a model of a tile's time in cycles: per K plane the
+// tensor core's 2 * bn or the arrival of its blocks (128 + bn / cg rows of 128 bytes at
+// about 40 bytes per cycle and SM), whichever is longer, plus the fill of the pipeline and
+// the epilogue, plus the exchange of a K split.
+W8Plan w8_plan_dense(int M, int NT, int G, int num_ctas) {
+    W8Plan best = {1, 128, 1};
+    long long best_cost = -1;
+    const auto consider = [&](int cg, int bn, int split) {
+        const long long tiles = (long long)ceil_div(M, bn) * ceil_div(NT, cg);
+        const long long slots = num_ctas / (cg * split);
+        if (slots < 1 || split > G || (split > 1 && tiles > slots)) return;
+        const int rows = 128 + bn / cg;
+        const long long plane = 2 * bn > rows * 16 / 5 ? 2 * bn : rows * 16 / 5;
+        const long long waves = (tiles + slots - 1) / slots;
+        const long long cost = waves * (ceil_div(G, split) * plane + 500) + 2500 + 8 * bn + (split > 1 ? 1200 + 8 * bn : 0);
+        if (best_cost < 0 || cost < best_cost) {
             best_cost = cost;
-            best = {2, bn};
+            best = {cg, bn, split};
         }
-    }
+    };
+    const int top = M < 128 ? round_up(M, 16) : 128;
+    for (int bn = top; bn >= 16; bn = bn > 16 && bn < 32 ? 16 : bn / 32 * 16)
+        for (int split = 1; split <= 8; split *= 2) consider(1, bn, split);
+    if (M > 64)
+        for (int bn = 256; bn >= 64; bn -= 32) consider(2, bn, 1);
     return best;
 }
 
-cudaError_t launch_gemm_w8a8(W8Args a, const W8Operands& op, int num_ctas, cudaStream_t stream) {
+cudaError_t launch_gemm_w8a8(W8Args a, const W8Operands& op, const W8Plan& plan, int num_ctas, cudaStream_t stream) {
     CUtensorMap mw, mx;
     cudaError_t e = make_map(&mw, op.wblocks, 128, (uint64_t)op.matrices * a.NT * a.G * kTileRows, 128, kTileRows, false);
     if (e != cudaSuccess) return e;
-    a.box_rows = op.cg == 1 ? 16 : 32;
+    a.BN = plan.bn;
+    a.box_rows = plan.cg == 1 ? 16 : 32;
     if (a.mt_tab != nullptr) {
         // tiled rows [G][rows][128]
         a.plane_x = 0;
@@ -616,7 +708,20 @@ cudaError_t launch_gemm_w8a8(W8Args a, const W8Operands& op, int num_ctas, cudaS
     }
     if (e != cudaSuccess) return e;
     a.pairs = a.ldo % 2 == 0 && reinterpret_cast<uintptr_t>(a.out) % 4 == 0;
-    return op.cg == 1 ? launch_instance<1>(mw, mx, a, num_ctas, stream) : launch_instance<2>(mw, mx, a, num_ctas, stream);
+    a.b_stage = (uint32_t)round_up(plan.bn / plan.cg, a.box_rows) * 128u;
+    a.recv = plan.split > 1 ? (uint32_t)(ceil_div(plan.bn, plan.split) * plan.split * kTileRows * 4) : 0u;
+    a.ns = (kW8SmemMax - kW8BarBytes - (int)a.recv) / (kW8BlockBytes + (int)a.b_stage);
+    if (a.ns > kW8MaxStages) a.ns = kW8MaxStages;
+    const int steps = ceil_div(a.G, plan.split);  // a short K needs no more stages
+    if (plan.split > 1 && a.ns > steps) a.ns = steps;
+    const int smem = w8_smem(a.ns, (int)a.b_stage, (int)a.recv);
+    if (num_ctas > kW8StatusWords) num_ctas = kW8StatusWords;
+    if (plan.split > 1) {
+        const int grid = ceil_div(a.M, plan.bn) * a.NT * plan.split;
+        return launch_instance<1, true>(mw, mx, a, smem, grid, plan.split, stream);
+    }
+    if (plan.cg == 1) return launch_instance<1, false>(mw, mx, a, smem, num_ctas, 1, stream);
+    return launch_instance<2, false>(mw, mx, a, smem, num_ctas / 2 * 2, 2, stream);
 }
 
 cudaError_t launch_pack_w8(const uint16_t* w, int E, int N, int K, int layout, uint8_t* packed, int8_t* codes, float* scale,

@@ -72,7 +72,7 @@ W4A8_EXPORT int w8a8_pack_weights(const void* w_bf16, int E, int N, int K, int l
 
 W4A8_EXPORT size_t w8a8_gemm_workspace_bytes(int M, int N, int K) {
     if (M < 0 || N < 1 || K < 1 || K > kW8MaxK) return 0;
-    return kAlign;  // the device error word
+    return kW8StatusWords * 4;  // one error word per CTA
 }
 
 W4A8_EXPORT int w8a8_gemm(const int8_t* qa, const float* sa, int M, const void* packed, int N, int K, const float* bias_opt,
@@ -90,9 +90,7 @@ W4A8_EXPORT int w8a8_gemm(const int8_t* qa, const float* sa, int M, const void* 
         const size_t el = out_type == W8A8_F32 || out_type == W8A8_I32 ? 4 : 2;
         if (!aligned(qa, 16) || !aligned(sa, 4) || !aligned(bias_opt, 4) || !aligned(y, el)) return W4A8_EALIGN;
     }
-    uint32_t* err = static_cast<uint32_t*>(ws);
-    W8_TRY(cudaMemsetAsync(err, 0, 16, s));
-    if (M == 0) return W4A8_OK;
+    if (M == 0) return to_status(cudaMemsetAsync(ws, 0, kW8StatusWords * 4, s));
     W8Args a{};
     W8Operands op{};
     a.NT = w8_tiles(N, W4A8_LAYOUT_PLAIN);
@@ -100,16 +98,13 @@ W4A8_EXPORT int w8a8_gemm(const int8_t* qa, const float* sa, int M, const void* 
     a.wscale = reinterpret_cast<const float*>(static_cast<const uint8_t*>(packed) + kHeaderBytes);
     a.act_scale = out_type == W8A8_I32 ? nullptr : sa;
     a.M = M;
-    const W8Plan plan = w8_plan_dense(M, a.NT, sm_count());
-    a.BN = plan.bn;
-    op.cg = plan.cg;
     a.mode = kW8Dense;
     a.out_type = out_type;
     a.out = y;
     a.ldo = N;
     a.nvalid = N;
     a.bias = out_type == W8A8_I32 ? nullptr : bias_opt;
-    a.err = err;
+    a.status = static_cast<uint32_t*>(ws);
     a.wait_limit = debug_wait_limit();
     a.debug = debug_flags();
     op.wblocks = static_cast<const uint8_t*>(packed) + w8_blocks_offset(1, a.NT);
@@ -117,8 +112,20 @@ W4A8_EXPORT int w8a8_gemm(const int8_t* qa, const float* sa, int M, const void* 
     op.x = qa;
     op.x_rows = M;
     ProfScope prof(W4A8_KERNEL_GEMM_DENSE, 1, s);
-    W8_TRY(launch_gemm_w8a8(a, op, sm_count(), s));
+    const int sms = sm_count();
+    W8_TRY(launch_gemm_w8a8(a, op, w8_plan_dense(M, a.NT, a.G, sms), sms, s));
     return W4A8_OK;
+}
+
+W4A8_EXPORT int w8a8_gemm_last_error(const void* ws, void* stream) {
+    if (ws == nullptr) return W4A8_EINVAL;
+    uint32_t v[kW8StatusWords];
+    cudaStream_t s = static_cast<cudaStream_t>(stream);
+    if (cudaMemcpyAsync(v, ws, sizeof v, cudaMemcpyDeviceToHost, s) != cudaSuccess) return W4A8_ECUDA;
+    if (cudaStreamSynchronize(s) != cudaSuccess) return W4A8_ECUDA;
+    uint32_t all = 0;
+    for (uint32_t w : v) all |= w;
+    return (int)all;
 }
 
 W4A8_EXPORT size_t w8a8_moe_workspace_bytes(int T, int E, int k, int H, int F) {
@@ -177,8 +184,6 @@ W4A8_EXPORT int w8a8_moe_forward(const void* packed_up, const void* packed_down,
     a.act_scale = s1;
     a.mt_tab = at<int4>(ws, L, R_MTTAB);
     a.n_mtiles = mtstart + E;
-    a.BN = plan.bn;
-    op.cg = plan.cg;
     a.mode = kW8Up;
     a.out_type = W8A8_BF16;
     a.out = h;
@@ -193,7 +198,7 @@ W4A8_EXPORT int w8a8_moe_forward(const void* packed_up, const void* packed_down,
     op.x_rows = L.R;
     {
         ProfScope p(W4A8_KERNEL_GEMM_UP, 1, st);
-        W8_TRY(launch_gemm_w8a8(a, op, sm_count(), st));
+        W8_TRY(launch_gemm_w8a8(a, op, plan, sm_count(), st));
     }
     {
         ProfScope p(W4A8_KERNEL_REQUANT, 1, st);
@@ -212,7 +217,7 @@ W4A8_EXPORT int w8a8_moe_forward(const void* packed_up, const void* packed_down,
     op.x = act2;
     {
         ProfScope p(W4A8_KERNEL_GEMM_DOWN, 1, st);
-        W8_TRY(launch_gemm_w8a8(a, op, sm_count(), st));
+        W8_TRY(launch_gemm_w8a8(a, op, plan, sm_count(), st));
     }
     {
         ProfScope p(W4A8_KERNEL_COMBINE, 1, st);

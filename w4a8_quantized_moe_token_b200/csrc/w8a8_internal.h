@@ -16,6 +16,7 @@ namespace w4a8 {
 // K plane), each row's 16-byte chunk c at chunk position c ^ (row & 7) (act_tiled_offset).
 constexpr int kW8BlockBytes = kTileRows * kGroup;
 constexpr uint32_t kW8PackMagic = 0x38413857u;  // "W8A8"
+constexpr int kW8StatusWords = 1024;
 constexpr int kW8MaxK = 1 << 17;                // 2^17 products of at most 2^14 stay below 2^31
 inline size_t w8_blocks_offset(int E, int NT) { return (size_t)kHeaderBytes + (size_t)E * NT * kTileRows * 4; }
 inline int w8_tiles(int N, int layout) {
@@ -32,18 +33,22 @@ struct W8Args {
     const int4* mt_tab;       // grouped: per row tile (expert, first row, rows, 0); dense: null
     const int* n_mtiles;      // grouped: number of row tiles (device)
     int M;                    // dense: rows
-    int BN;                   // tokens per row tile at most
+    int BN;                   // tokens per row tile at most (the plan's)
     int mode;                 // kW8Dense / kW8Down: scaled output of out_type; kW8Up: SwiGLU -> bf16 h
     int out_type;             // W8A8_F32, ...
     void* out;
     int ldo;
     int nvalid;               // valid output columns (N, or F for kW8Up)
     const float* bias;        // optional, [nvalid]
-    uint32_t* err;            // device error word
+    uint32_t* err;            // device error word (grouped), or null and
+    uint32_t* status;         // kW8StatusWords words, one per CTA (dense), or null
     long long wait_limit;     // clock cycles a bounded wait may last
     uint32_t debug;           // test hook
-    int pairs;                // 16-bit rows may be stored two columns at a time (set by the launcher)
-    int box_rows;             // token rows per tensor-map box (set by the launcher)
+    // set by the launcher
+    int pairs;                // 16-bit rows may be stored two columns at a time
+    int ns;                   // shared-memory stages
+    uint32_t b_stage, recv;   // bytes of a stage's token block and of the K split's receive buffer
+    int box_rows;             // token rows per tensor-map box
     int plane_x, plane_y;     // tensor-map coordinates of K plane g: (g * plane_x, row + g * plane_y)
 };
 
@@ -53,20 +58,20 @@ struct W8Operands {
     int matrices;             // number of weight matrices
     const int8_t* x;          // dense: rows of G * 128 bytes; grouped: tiled rows [G][x_rows][128]
     int x_rows;
-    int cg;                   // CTAs per tile (W8Plan)
 };
 
-// Tile shape: cg CTAs work on cg * 128 channels x up to bn tokens.
+// Tile shape: cg CTAs work on cg * 128 channels x up to bn tokens; split > 1 (cg = 1, dense):
+// as many CTAs share a tile's K planes.
 struct W8Plan {
-    int cg, bn;
+    int cg, bn, split;
 };
 
-// ... for a dense layer of M rows and NT weight tiles on num_ctas SMs
-W8Plan w8_plan_dense(int M, int NT, int num_ctas);
+// the tile shape for a dense layer of M rows, NT weight tiles and G K planes on num_ctas SMs
+W8Plan w8_plan_dense(int M, int NT, int G, int num_ctas);
 // ... for a grouped layer with this mean number of tokens per expert; the permutation's
 // row-tile table must be built with bn
 W8Plan w8_plan_grouped(int avg_tokens);
-cudaError_t launch_gemm_w8a8(W8Args a, const W8Operands& op, int num_ctas, cudaStream_t stream);
+cudaError_t launch_gemm_w8a8(W8Args a, const W8Operands& op, const W8Plan& plan, int num_ctas, cudaStream_t stream);
 cudaError_t launch_pack_w8(const uint16_t* w, int E, int N, int K, int layout, uint8_t* packed, int8_t* codes, float* scale,
                            cudaStream_t stream);
 
