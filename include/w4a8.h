@@ -150,7 +150,8 @@ int w4a8_route_topk(const void* logits_bf16, int T, int E, int k, int32_t* ids, 
  *           score is its largest c or, with W4A8_ROUTE_GROUP_TOP2, the sum of its two largest;
  *           only experts of the topk_group best groups (ties to the lower group) are eligible;
  *   ids[t]= the k largest c of the eligible experts, largest first, ties to the lower id;
- *   w[t][j] = s[ids[t][j]], with W4A8_ROUTE_RENORM divided by their sum, times `scale`.
+ *   w[t][j] = s[ids[t][j]], with W4A8_ROUTE_RENORM divided by their sum (which the chosen
+ *           logits alone determine: no underflow of the scores enters), times `scale`.
  * Scores are compared as 64-bit values, so that ids do not depend on fp32 rounding.
  * An expert whose logit is -inf or NaN, or whose bias is, is masked: it ranks after every
  * other one (ties to the lower id), adds nothing to its group's score and, should it fill a

@@ -119,6 +119,12 @@ def route_experts(logits, k, sigmoid=False, renorm=False, top2=False, bias=None,
         ids[t] = chosen
         wt = np.array([s[e] if usable[e] else 0.0 for e in chosen])
         if renorm:
-            wt = wt / wt.sum() if wt.sum() > 0 else np.zeros(k)
+            # s_j / sum s_i over the chosen; the scores relative to the largest one's exponential,
+            # so that neither a common factor (the softmax's sum) nor underflow enters
+            got = [e for e in chosen if usable[e]]
+            z = [min(v[e], 0.0) if sigmoid else v[e] for e in got]
+            rel = {e: (1.0 if z[i] == max(z) else np.exp(z[i] - max(z))) / (1.0 + np.exp(-abs(v[e])) if sigmoid else 1.0)
+                   for i, e in enumerate(got)}
+            wt = np.array([rel[e] / sum(rel.values()) if e in rel else 0.0 for e in chosen])
         w[t] = wt * scale
     return ids, w

@@ -130,6 +130,17 @@ def test_extreme_logits_and_scales():
         check(x, 5, sigmoid, bias=torch.linspace(-1e30, 1e30, 8), scale=0.0)
 
 
+def test_renormalised_weights_of_tiny_scores():
+    # sigmoid of -100 is 4e-44 and the softmax's share of a masked-off top 1e-44: the ratios hold
+    x = logits_of(41, 20, 32, "fp32")
+    check(x - 100.0, 5, sigmoid=True, renorm=True)
+    check(x - 300.0, 5, sigmoid=True, renorm=True)
+    x[:, 9] = 100.0
+    bias = torch.zeros(32)
+    bias[9] = -torch.inf
+    check(x, 5, renorm=True, bias=bias)
+
+
 def test_empty_batch_and_refused_tensors():
     ids = torch.empty((0, 4), dtype=torch.int32, device="cuda")
     w = torch.empty((0, 4), dtype=torch.float32, device="cuda")
