@@ -220,7 +220,8 @@ __device__ __forceinline__ uint16_t to_bits16(float v, int type) {
 // split, no workspace and no second launch.
 template <int CG, bool kSplit>
 __global__ void __launch_bounds__(kW8Threads, 1)
-    gemm_w8a8_kernel(const __grid_constant__ CUtensorMap map_w, const __grid_constant__ CUtensorMap map_x, const W8Args a) {
+    gemm_w8a8_kernel(const __grid_constant__ CUtensorMap map_w, const __grid_constant__ CUtensorMap map_x,
+                     const __grid_constant__ CUtensorMap map_small, const W8Args a) {
     constexpr uint32_t kAccCols = 128 * CG;  // columns of one of the two accumulators
     extern __shared__ uint8_t smem_raw[];
     const uint32_t raw_addr = smem_u32(smem_raw);
@@ -274,8 +275,14 @@ __global__ void __launch_bounds__(kW8Threads, 1)
                 // this CTA's token rows: all of them, or half of the tile's N
                 const int rows = CG == 1 ? t.nrows : round_up(t.nrows, 32) / 2;
                 const int row0 = t.row0 + (int)rank * rows;
-                const int boxes = ceil_div(rows, a.box_rows);
-                const uint32_t bytes = (uint32_t)kW8BlockBytes + (uint32_t)(boxes * a.box_rows) * 128u;
+                // one box for a whole tile (every copy costs the producer and the TMA unit as
+                // much as some KB of data: 256-token tiles in 32-row boxes ran at 2490 TOPS, in
+                // one box at 3240), up to two small ones for the few rows of a ragged tile
+                const bool small = rows <= 2 * a.small_rows;
+                const CUtensorMap* map = small ? &map_small : &map_x;
+                const int box_rows = small ? a.small_rows : a.box_rows;
+                const int boxes = small ? ceil_div(rows, box_rows) : 1;
+                const uint32_t bytes = (uint32_t)kW8BlockBytes + (uint32_t)(boxes * box_rows) * 128u;
                 // (a pair's second tile may lie past the last one: read that one again)
                 const int wrow = (t.e * a.NT + min(t.nt, a.NT - 1)) * a.G * kTileRows;
                 for (int g = g0; g < g1; ++g, ++j) {
@@ -288,8 +295,8 @@ __global__ void __launch_bounds__(kW8Threads, 1)
                     const auto load = CG == 1 ? tma_load_2d : tma_load_2d_pair;
                     load(sA + s * kW8BlockBytes, &map_w, 0, wrow + g * kTileRows, bar);
                     for (int b = 0; b < boxes; ++b)
-                        load(sB + s * a.b_stage + (uint32_t)(b * a.box_rows) * 128u, &map_x, g * a.plane_x,
-                             row0 + b * a.box_rows + g * a.plane_y, bar);
+                        load(sB + s * a.b_stage + (uint32_t)(b * box_rows) * 128u, map, g * a.plane_x,
+                             row0 + b * box_rows + g * a.plane_y, bar);
                 }
             }
             // Never leave with a copy or a barrier arrival still on its way into this CTA's
@@ -608,7 +615,7 @@ cudaError_t make_map(CUtensorMap* m, const void* base, uint64_t width, uint64_t 
 namespace {
 
 template <int CG, bool kSplit>
-cudaError_t launch_instance(const CUtensorMap& mw, const CUtensorMap& mx, const W8Args& a, int smem, int grid, int cluster,
+cudaError_t launch_instance(const CUtensorMap& mw, const CUtensorMap& mx, const CUtensorMap& ms, const W8Args& a, int smem, int grid, int cluster,
                             cudaStream_t stream) {
     const auto kernel = gemm_w8a8_kernel<CG, kSplit>;
     static std::mutex mu;
@@ -649,7 +656,7 @@ cudaError_t launch_instance(const CUtensorMap& mw, const CUtensorMap& mx, const 
         }
         if (CG == 2 && grid > clusters[dev] * CG) cfg.gridDim = clusters[dev] * CG;
     }
-    return cudaLaunchKernelEx(&cfg, kernel, mw, mx, a);
+    return cudaLaunchKernelEx(&cfg, kernel, mw, mx, ms, a);
 }
 
 }  // namespace
@@ -690,25 +697,29 @@ W8Plan w8_plan_dense(int M, int NT, int G, int num_ctas) {
 }
 
 cudaError_t launch_gemm_w8a8(W8Args a, const W8Operands& op, const W8Plan& plan, int num_ctas, cudaStream_t stream) {
-    CUtensorMap mw, mx;
+    CUtensorMap mw, mx, ms;
     cudaError_t e = make_map(&mw, op.wblocks, 128, (uint64_t)op.matrices * a.NT * a.G * kTileRows, 128, kTileRows, false);
     if (e != cudaSuccess) return e;
     a.BN = plan.bn;
-    a.box_rows = plan.cg == 1 ? 16 : 32;
+    a.box_rows = plan.bn / plan.cg;  // 16 .. 128, a multiple of 16
+    a.small_rows = 16;
     if (a.mt_tab != nullptr) {
         // tiled rows [G][rows][128]
         a.plane_x = 0;
         a.plane_y = op.x_rows;
         e = make_map(&mx, op.x, 128, (uint64_t)op.x_rows * a.G, 128, (uint32_t)a.box_rows, false);
+        if (e == cudaSuccess) e = make_map(&ms, op.x, 128, (uint64_t)op.x_rows * a.G, 128, (uint32_t)a.small_rows, false);
     } else {
         // row-major rows of G * 128 bytes
         a.plane_x = 128;
         a.plane_y = 0;
         e = make_map(&mx, op.x, (uint64_t)a.G * 128, (uint64_t)op.x_rows, (uint64_t)a.G * 128, (uint32_t)a.box_rows, true);
+        ms = mx;
+        a.small_rows = 0;  // (rows past M are not read: the box costs what it holds)
     }
     if (e != cudaSuccess) return e;
     a.pairs = a.ldo % 2 == 0 && reinterpret_cast<uintptr_t>(a.out) % 4 == 0;
-    a.b_stage = (uint32_t)round_up(plan.bn / plan.cg, a.box_rows) * 128u;
+    a.b_stage = (uint32_t)a.box_rows * 128u;
     a.recv = plan.split > 1 ? (uint32_t)(ceil_div(plan.bn, plan.split) * plan.split * kTileRows * 4) : 0u;
     a.ns = (kW8SmemMax - kW8BarBytes - (int)a.recv) / (kW8BlockBytes + (int)a.b_stage);
     if (a.ns > kW8MaxStages) a.ns = kW8MaxStages;
@@ -718,10 +729,10 @@ cudaError_t launch_gemm_w8a8(W8Args a, const W8Operands& op, const W8Plan& plan,
     if (num_ctas > kW8StatusWords) num_ctas = kW8StatusWords;
     if (plan.split > 1) {
         const int grid = ceil_div(a.M, plan.bn) * a.NT * plan.split;
-        return launch_instance<1, true>(mw, mx, a, smem, grid, plan.split, stream);
+        return launch_instance<1, true>(mw, mx, ms, a, smem, grid, plan.split, stream);
     }
-    if (plan.cg == 1) return launch_instance<1, false>(mw, mx, a, smem, num_ctas, 1, stream);
-    return launch_instance<2, false>(mw, mx, a, smem, num_ctas / 2 * 2, 2, stream);
+    if (plan.cg == 1) return launch_instance<1, false>(mw, mx, ms, a, smem, num_ctas, 1, stream);
+    return launch_instance<2, false>(mw, mx, ms, a, smem, num_ctas / 2 * 2, 2, stream);
 }
 
 cudaError_t launch_pack_w8(const uint16_t* w, int E, int N, int K, int layout, uint8_t* packed, int8_t* codes, float* scale,

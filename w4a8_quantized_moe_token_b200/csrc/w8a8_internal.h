@@ -48,7 +48,7 @@ struct W8Args {
     int pairs;                // 16-bit rows may be stored two columns at a time
     int ns;                   // shared-memory stages
     uint32_t b_stage, recv;   // bytes of a stage's token block and of the K split's receive buffer
-    int box_rows;             // token rows per tensor-map box
+    int box_rows, small_rows; // token rows of the tile's tensor-map box and of the small one (0: none)
     int plane_x, plane_y;     // tensor-map coordinates of K plane g: (g * plane_x, row + g * plane_y)
 };
 
