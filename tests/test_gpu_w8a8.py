@@ -76,7 +76,9 @@ def test_pack_is_bit_exact(E, N, K, layout):
 SHAPES = [(1, 1, 1), (1, 128, 128), (1, 4096, 2048), (3, 127, 100), (15, 129, 384), (16, 256, 512), (17, 384, 200),
           (32, 640, 4096), (33, 130, 1024), (64, 2048, 4096), (100, 131, 640), (127, 512, 256), (128, 256, 7168),
           (129, 1411, 1000), (200, 320, 1152), (255, 300, 130), (256, 1024, 1024), (257, 768, 896), (511, 96, 2056),
-          (700, 2304, 512), (1500, 1000, 264), (2500, 4104, 136), (5, 20000, 256), (9, 256, 20000)]
+          (700, 2304, 512), (1500, 1000, 264), (2500, 4104, 136), (5, 20000, 256), (9, 256, 20000),
+          # tiles of two halves: full, ragged, with one token in the second, a short and a long K
+          (4096, 4864, 384), (5000, 5000, 640), (16385, 1152, 128), (9217, 2432, 1536)]
 
 
 def dense_case(M, N, K, seed=0, bias=False):
@@ -248,6 +250,7 @@ LAYERS = [
     (130, 2, 1, 264, 70, "uniform"), (333, 3, 2, 384, 200, "zipf"), (600, 4, 2, 256, 256, "uniform"),
     (900, 4, 3, 520, 130, "zipf"), (2100, 6, 2, 128, 64, "uniform"), (3000, 3, 2, 384, 136, "uniform"),
     (20, 200, 8, 128, 64, "uniform"),
+    (1500, 3, 2, 256, 320, "uniform"), (1100, 2, 2, 640, 64, "zipf"), (2500, 4, 2, 136, 96, "zipf"),
 ]
 
 

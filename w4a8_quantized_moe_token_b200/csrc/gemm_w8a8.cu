@@ -19,8 +19,9 @@
 // that a step of 2 x 128 x 256 x 128 products reads 32 KB per SM instead of the 48 KB that
 // 128 x 256 alone would: at full rate (512 cycles a step) 64 bytes per cycle and SM.
 //
-// One persistent CTA per SM: a producer warp (TMA), an MMA warp (one elected thread issues,
-// in the pair's first CTA) and 8 epilogue warps.  Steps are 128-wide K planes; two
+// One persistent CTA per SM: producer warps (TMA; a thread's time per step is a fixed few
+// hundred cycles, longer than a step's arithmetic, so they take steps in turn), an MMA warp
+// (one elected thread issues, in the pair's first CTA) and 8 epilogue warps.  Steps are 128-wide K planes; two
 // accumulators, so that a tile's epilogue overlaps the next tile's K loop.  Every wait is
 // bounded.
 #include <cuda.h>
@@ -36,9 +37,10 @@ namespace w4a8 {
 namespace {
 
 constexpr int kW8EpiWarps = 8;
+constexpr int kW8Producers = 2;
 constexpr int kW8ProdWarp = kW8EpiWarps;
-constexpr int kW8MmaWarp = kW8EpiWarps + 1;
-constexpr int kW8Threads = 32 * (kW8EpiWarps + 2);
+constexpr int kW8MmaWarp = kW8ProdWarp + kW8Producers;
+constexpr int kW8Threads = 32 * (kW8MmaWarp + 1);
 constexpr int kW8MaxStages = 12;
 // shared memory: ns weight blocks, ns token blocks (both 1024-aligned: swizzle atoms), the
 // receive buffer of a K split, barriers (full, empty, 2 x accumulator full / empty, receive)
@@ -127,6 +129,19 @@ __device__ __forceinline__ bool mbar_try_wait_cluster(uint32_t bar, uint32_t par
         "selp.b32 %0, 1, 0, p;\n\t}"
         : "=r"(ok)
         : "r"(bar), "r"(parity), "r"(20000u)
+        : "memory");
+    return ok != 0;
+}
+template <bool kCluster>
+__device__ __forceinline__ bool w8_test(uint32_t bar, uint32_t parity) {
+    if (!kCluster) return mbar_test(bar, parity);
+    uint32_t ok;
+    asm volatile(
+        "{\n\t.reg .pred p;\n\t"
+        "mbarrier.test_wait.parity.acquire.cluster.shared::cta.b64 p, [%1], %2;\n\t"
+        "selp.b32 %0, 1, 0, p;\n\t}"
+        : "=r"(ok)
+        : "r"(bar), "r"(parity)
         : "memory");
     return ok != 0;
 }
@@ -265,8 +280,9 @@ __global__ void __launch_bounds__(kW8Threads, 1)
     const int g1 = kSplit ? (int)((long long)a.G * (part + 1) / parts) : a.G;
     const int u0 = (int)(blockIdx.x / (CG * parts)), du = (int)(gridDim.x / (CG * parts));
 
-    if (warp == kW8ProdWarp) {
-        // ---------------- producer ----------------
+    if (warp >= kW8ProdWarp && warp < kW8MmaWarp) {
+        // ---------------- producers: warp pi takes the steps j with j % kW8Producers == pi ----------------
+        const uint32_t pi = (uint32_t)(warp - kW8ProdWarp);
         if (lane == 0) {
             uint32_t j = 0, s = 0, ph = 0;  // step, its stage and the stage's phase
             bool ok = true;
@@ -287,6 +303,7 @@ __global__ void __launch_bounds__(kW8Threads, 1)
                 const int wrow = (t.e * a.NT + min(t.nt, a.NT - 1)) * a.G * kTileRows;
                 for (int g = g0; g < g1; ++g, ++j) {
                     if (j > 0 && ++s == NS) { s = 0; ph ^= 1u; }
+                    if (j % kW8Producers != pi) continue;
                     if (!w8_wait(empty + 8 * s, ph ^ 1u, abort_flag, a.err, a.wait_limit)) { ok = false; break; }
                     // test hook: leave the first step's stage empty, so that its consumers time out
                     if (j == 0 && blockIdx.x == 0 && (a.debug & kDebugSkipFirstCopy)) continue;
@@ -304,6 +321,7 @@ __global__ void __launch_bounds__(kW8Threads, 1)
             // timeout) the MMAs that read them have reported back.
             const uint32_t first = j > NS ? j - NS : 0u;
             for (uint32_t q = first; q < j; ++q) {
+                if (q % kW8Producers != pi) continue;
                 if (rank == 0) w8_drain(full + 8 * (q % NS), (q / NS) & 1u, a.wait_limit);
                 if (ok && !*abort_flag) w8_drain(empty + 8 * (q % NS), (q / NS) & 1u, a.wait_limit);
             }
@@ -312,7 +330,7 @@ __global__ void __launch_bounds__(kW8Threads, 1)
     } else if (warp == kW8MmaWarp) {
         // ---------------- MMA issue (the pair's first CTA) ----------------
         uint32_t s = 0, ph = 0, tile = 0;
-        bool ok = rank == 0;
+        bool ok = rank == 0, ready = false;  // ready: an early test found this step's stage full
         for (int u = u0; u < total && ok; u += du, ++tile) {
             const W8Tile t = w8_tile<CG>(u, a, rank);
             const uint32_t idesc = idesc_i8(128 * CG, round_up(t.nrows, 16 * CG));
@@ -321,18 +339,20 @@ __global__ void __launch_bounds__(kW8Threads, 1)
             if (!w8_wait<CG == 2>(dempty + 8 * b, ((tile >> 1) & 1u) ^ 1u, abort_flag, a.err, a.wait_limit)) break;
             tc_fence_after();
             for (int g = g0; g < g1; ++g) {
-                if (!w8_wait<CG == 2>(full + 8 * s, ph, abort_flag, a.err, a.wait_limit)) { ok = false; break; }
+                if (!ready && !w8_wait<CG == 2>(full + 8 * s, ph, abort_flag, a.err, a.wait_limit)) { ok = false; break; }
+                const uint32_t s0 = s;
+                if (++s == NS) { s = 0; ph ^= 1u; }
+                ready = w8_test<CG == 2>(full + 8 * s, ph);
                 tc_fence_after();
                 if (elect_one()) {
 #pragma unroll
                     for (uint32_t kk = 0; kk < 4; ++kk)
-                        mma_i8_ss<CG>(d, smem_desc_sw128(sA + s * kW8BlockBytes + kk * 32),
-                                      smem_desc_sw128(sB + s * a.b_stage + kk * 32), idesc, g != g0 || kk != 0);
-                    w8_commit<CG>(empty + 8 * s);
+                        mma_i8_ss<CG>(d, smem_desc_sw128(sA + s0 * kW8BlockBytes + kk * 32),
+                                      smem_desc_sw128(sB + s0 * a.b_stage + kk * 32), idesc, g != g0 || kk != 0);
+                    w8_commit<CG>(empty + 8 * s0);
                     if (g == g1 - 1) w8_commit<CG>(dfull + 8 * b);
                 }
                 __syncwarp();
-                if (++s == NS) { s = 0; ph ^= 1u; }
             }
         }
     } else {
