@@ -44,7 +44,7 @@ constexpr int kW8Threads = 32 * (kW8MmaWarp + 1);
 constexpr int kW8MaxStages = 12;
 // shared memory: ns weight blocks, ns token blocks (both 1024-aligned: swizzle atoms), the
 // receive buffer of a K split, barriers (full, empty, 2 x accumulator full / empty, receive)
-constexpr int kW8BarBytes = (2 * kW8MaxStages + 5) * 8 + 16;
+constexpr int kW8BarBytes = (2 * kW8MaxStages + 5) * 8 + 16 + 64 * 4;  // + the K split's token scales
 constexpr int kW8SmemMax = 227 * 1024 - 1024;  // without the alignment slack
 inline int w8_smem(int ns, int b_stage, int recv) { return ns * (kW8BlockBytes + b_stage) + recv + kW8BarBytes + 1024; }
 
@@ -111,8 +111,11 @@ __device__ __forceinline__ uint32_t cluster_size() {
 }
 __device__ __forceinline__ void cluster_arrive() { asm volatile("barrier.cluster.arrive.release;" ::: "memory"); }
 __device__ __forceinline__ void cluster_wait() { asm volatile("barrier.cluster.wait.acquire;" ::: "memory"); }
-__device__ __forceinline__ void st_cluster(uint32_t cluster_addr, uint32_t v) {
-    asm volatile("st.shared::cluster.u32 [%0], %1;" ::"r"(cluster_addr), "r"(v) : "memory");
+// store into another CTA's shared memory, reported to that CTA's barrier as 4 bytes
+__device__ __forceinline__ void st_async(uint32_t cluster_addr, uint32_t v, uint32_t cluster_bar) {
+    asm volatile("st.async.shared::cluster.mbarrier::complete_tx::bytes.b32 [%0], %1, [%2];" ::"r"(cluster_addr), "r"(v),
+                 "r"(cluster_bar)
+                 : "memory");
 }
 __device__ __forceinline__ void cluster_sync() {
     asm volatile("barrier.cluster.arrive.release.aligned;\n\tbarrier.cluster.wait.acquire.aligned;" ::: "memory");
@@ -231,7 +234,8 @@ __device__ __forceinline__ uint16_t to_bits16(float v, int type) {
 
 // kSplit (CG = 1, dense): the CTAs of a cluster share one tile, each taking a part of its K
 // planes.  Every CTA sends the INT32 partials of its peers' tokens into their shared memory
-// and finishes its own share of the tokens: exact sums, so the result does not depend on the
+// (st.async, counted by the receiver's barrier) and finishes its own share of the tokens:
+// exact sums, so the result does not depend on the
 // split, no workspace and no second launch.
 template <int CG, bool kSplit>
 __global__ void __launch_bounds__(kW8Threads, 1)
@@ -261,9 +265,14 @@ __global__ void __launch_bounds__(kW8Threads, 1)
             mbar_init(dfull + 8 * b, 1);
             mbar_init(dempty + 8 * b, kW8EpiWarps * CG);  // in the first CTA, from both
         }
-        if (kSplit) mbar_init(recv_full, kW8EpiWarps * parts);
+        if (kSplit) mbar_init(recv_full, 1);
         *abort_flag = 0;
         fence_mbar_init();
+    }
+    if (warp == kW8ProdWarp && lane < 2) {
+        // the maps' first use would wait for them
+        if (lane == 0) asm volatile("prefetch.tensormap [%0];" ::"l"(&map_w) : "memory");
+        if (lane == 1) asm volatile("prefetch.tensormap [%0];" ::"l"(&map_x) : "memory");
     }
     if (warp == kW8MmaWarp) w8_tmem_alloc<CG>(smem_u32(tmem_slot), 2 * kAccCols);
     tc_fence_before();
@@ -273,6 +282,7 @@ __global__ void __launch_bounds__(kW8Threads, 1)
     tc_fence_after();
     const uint32_t tmem = *tmem_slot;
 
+    grid_dep_launch();
     grid_dep_wait();  // the previous kernel on the stream has completed
     const int total = ceil_div(a.NT, CG) * (a.mt_tab != nullptr ? __ldg(a.n_mtiles) : ceil_div(a.M, a.BN));
     // this CTA's K planes [g0, g1) of a tile; kSplit: one tile per cluster
@@ -300,7 +310,8 @@ __global__ void __launch_bounds__(kW8Threads, 1)
                 const int boxes = small ? ceil_div(rows, box_rows) : 1;
                 const uint32_t bytes = (uint32_t)kW8BlockBytes + (uint32_t)(boxes * box_rows) * 128u;
                 // (a pair's second tile may lie past the last one: read that one again)
-                const int wrow = (t.e * a.NT + min(t.nt, a.NT - 1)) * a.G * kTileRows;
+                const int wunit = (t.e * a.NT + min(t.nt, a.NT - 1)) * a.G * (kTileRows / 16);
+                const int unit0 = row0 / a.row_unit, box_units = box_rows / a.row_unit;
                 for (int g = g0; g < g1; ++g, ++j) {
                     if (j > 0 && ++s == NS) { s = 0; ph ^= 1u; }
                     if (j % kW8Producers != pi) continue;
@@ -310,10 +321,10 @@ __global__ void __launch_bounds__(kW8Threads, 1)
                     if (rank == 0) mbar_arrive_expect_tx(full + 8 * s, bytes * CG);
                     const uint32_t bar = CG == 1 ? full + 8 * s : mapa(full + 8 * s, 0);
                     const auto load = CG == 1 ? tma_load_2d : tma_load_2d_pair;
-                    load(sA + s * kW8BlockBytes, &map_w, 0, wrow + g * kTileRows, bar);
+                    load(sA + s * kW8BlockBytes, &map_w, 0, wunit + g * (kTileRows / 16), bar);
                     for (int b = 0; b < boxes; ++b)
                         load(sB + s * a.b_stage + (uint32_t)(b * box_rows) * 128u, map, g * a.plane_x,
-                             row0 + b * box_rows + g * a.plane_y, bar);
+                             unit0 + b * box_units + g * a.plane_y, bar);
                 }
             }
             // Never leave with a copy or a barrier arrival still on its way into this CTA's
@@ -369,18 +380,36 @@ __global__ void __launch_bounds__(kW8Threads, 1)
             // output column: channel n (past the last tile: none valid)
             const int n = a.mode == kW8Up ? t.nt * (kTileRows / 2) + (r >> 1) : t.nt * kTileRows + r;
             const float bias = (a.bias != nullptr && n < a.nvalid) ? __ldg(a.bias + n) : 0.f;
+            // token scales, ahead of the accumulator: kSplit, those of this CTA's tokens in shared
+            // memory; otherwise lane l's of each chunk of 32 tokens in a register
+            float* sa_s = reinterpret_cast<float*>(smem + (recv_full + 16 - base));
+            float sa_r[CG * 2];
+            if (kSplit) {
+                const int tok = (int)part * ceil_div(t.nrows, (int)parts) + (int)threadIdx.x;
+                if (threadIdx.x < 64) sa_s[threadIdx.x] = a.act_scale != nullptr && tok < t.nrows ? __ldg(a.act_scale + t.row0 + tok) : 0.f;
+                named_bar_sync(1, kW8EpiWarps * 32);
+            } else {
+#pragma unroll
+                for (int c = 0; c < CG * 2; ++c) {
+                    const int tok = half * 32 + c * 64 + lane;
+                    sa_r[c] = a.act_scale != nullptr && tok < t.nrows ? __ldg(a.act_scale + t.row0 + tok) : 0.f;
+                }
+            }
             if (!w8_wait(dfull + 8 * b, (tile >> 1) & 1u, abort_flag, a.err, a.wait_limit)) break;
             tc_fence_after();
             if (kSplit) {
                 // tokens [p * per, (p + 1) * per) are finished by CTA p, which keeps the
                 // partials of source s at recv[s][token][channel]
                 const int per = ceil_div(t.nrows, (int)parts);
+                const int first = (int)part * per, count = max(0, min(per, t.nrows - first));
+                if (threadIdx.x == 0) mbar_arrive_expect_tx(recv_full, parts * (uint32_t)count * (kTileRows * 4u));
                 for (int c0 = half * 32; c0 < t.nrows; c0 += 64) {
                     uint32_t v[32];
                     tmem_ld32(tmem + ((uint32_t)(q * 32) << 16) + (uint32_t)c0, v);
                     tmem_ld_wait();
                     int p = c0 / per, left = (p + 1) * per - c0;  // tokens left for CTA p
                     uint32_t dst = mapa(recv, (uint32_t)p) + (uint32_t)(((int)part * per + c0 - p * per) * kTileRows + r) * 4u;
+                    uint32_t bar = mapa(recv_full, (uint32_t)p);
 #pragma unroll
                     for (int i = 0; i < 32; ++i) {
                         if (c0 + i < t.nrows) {
@@ -388,31 +417,26 @@ __global__ void __launch_bounds__(kW8Threads, 1)
                                 ++p;
                                 left = per;
                                 dst = mapa(recv, (uint32_t)p) + (uint32_t)((int)part * per * kTileRows + r) * 4u;
+                                bar = mapa(recv_full, (uint32_t)p);
                             }
-                            st_cluster(dst, v[i]);
+                            st_async(dst, v[i], bar);
                             dst += kTileRows * 4;
                             --left;
                         }
                     }
                 }
-                __syncwarp();
-                if (lane < (int)parts) {
-                    asm volatile("fence.acq_rel.cluster;" ::: "memory");
-                    mbar_arrive_cluster(mapa(recv_full, (uint32_t)lane));
-                }
-                __syncwarp();
                 if (!w8_wait<true>(recv_full, 0, abort_flag, a.err, a.wait_limit)) break;
-                const int first = (int)part * per, count = min(per, t.nrows - first);
                 const int32_t* rb = reinterpret_cast<const int32_t*>(smem + (recv - base)) + r;
                 for (int i = half; i < count; i += 2) {
                     int sum = 0;
                     for (uint32_t src = 0; src < parts; ++src) sum += rb[((int)src * per + i) * kTileRows];
+                    const float sa = sa_s[i];
                     const size_t at = (size_t)(t.row0 + first + i) * a.ldo + n;
                     if (n < a.nvalid) {
                         if (a.out_type == W8A8_I32) {
                             static_cast<int32_t*>(a.out)[at] = sum;
                         } else {
-                            const float y = __int2float_rn(sum) * (sw * __ldg(a.act_scale + t.row0 + first + i)) + bias;
+                            const float y = __int2float_rn(sum) * (sw * sa) + bias;
                             if (a.out_type == W8A8_F32)
                                 static_cast<float*>(a.out)[at] = y;
                             else
@@ -422,9 +446,12 @@ __global__ void __launch_bounds__(kW8Threads, 1)
                 }
                 break;
             }
-            for (int c0 = half * 32; c0 < t.nrows; c0 += 64) {
+#pragma unroll
+            for (int c = 0; c < CG * 2; ++c) {
+                const int c0 = half * 32 + c * 64;
+                if (c0 >= t.nrows) break;
                 const int ncol = min(32, t.nrows - c0);  // tokens of this chunk
-                const float sa = lane < ncol && a.act_scale != nullptr ? __ldg(a.act_scale + t.row0 + c0 + lane) : 0.f;
+                const float sa = sa_r[c];
                 uint32_t v[32];
                 tmem_ld32(tmem + ((uint32_t)(q * 32) << 16) + b * kAccCols + (uint32_t)c0, v);
                 tmem_ld_wait();
@@ -490,9 +517,11 @@ __global__ void __launch_bounds__(kW8Threads, 1)
 
     __syncthreads();
     if (kSplit && warp >= kW8ProdWarp) cluster_wait();  // (the epilogue warps have waited)
-    if (CG == 2 || kSplit) {
-        // after a timeout the pair's copies and arrivals are not accounted for: give them
-        // ample time (50 us) to land before either CTA's shared memory goes away
+    if (CG == 2 || (kSplit && *abort_flag)) {
+        // after a timeout the cluster's copies, stores and arrivals are not accounted for: give
+        // them ample time (50 us) to land before this CTA's shared memory goes away, and stay
+        // until every other CTA has come this far or left.  (kSplit without one: a CTA has
+        // received all that is sent to it before it leaves.)
         if (*abort_flag) {
             const long long t0 = clock64();
             while (clock64() - t0 < 100000) {
@@ -616,16 +645,30 @@ EncodeFn encode_fn() {
     return fn;
 }
 
-// rows of `width` bytes, `pitch` bytes apart, copied in boxes of 128 bytes x box_rows
-cudaError_t make_map(CUtensorMap* m, const void* base, uint64_t width, uint64_t rows, uint64_t pitch, uint32_t box_rows,
-                     bool swizzle) {
+// Row-major INT8 rows of `width` bytes (a multiple of 128), copied in boxes of 128 bytes x
+// box_rows and swizzled on the way.
+cudaError_t make_map_rows(CUtensorMap* m, const void* base, uint64_t width, uint64_t rows, uint32_t box_rows) {
     const EncodeFn fn = encode_fn();
     if (fn == nullptr) return cudaErrorNotSupported;
-    const cuuint64_t dims[2] = {width, rows}, strides[1] = {pitch};
+    const cuuint64_t dims[2] = {width, rows}, strides[1] = {width};
     const cuuint32_t box[2] = {128, box_rows}, steps[2] = {1, 1};
     return fn(m, CU_TENSOR_MAP_DATA_TYPE_UINT8, 2, const_cast<void*>(base), dims, strides, box, steps,
-              CU_TENSOR_MAP_INTERLEAVE_NONE, swizzle ? CU_TENSOR_MAP_SWIZZLE_128B : CU_TENSOR_MAP_SWIZZLE_NONE,
-              CU_TENSOR_MAP_L2_PROMOTION_L2_128B, CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS
+              CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_128B, CU_TENSOR_MAP_L2_PROMOTION_L2_128B,
+              CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS
+               ? cudaSuccess
+               : cudaErrorInvalidValue;
+}
+
+// Contiguous memory in units of 2 KB (16 tile rows of 128 bytes), copied `box` units at a
+// time.  (The TMA unit's time goes by the box's rows: 2 KB rows, of 8-byte elements.)
+cudaError_t make_map_linear(CUtensorMap* m, const void* base, uint64_t units, uint32_t box) {
+    const EncodeFn fn = encode_fn();
+    if (fn == nullptr) return cudaErrorNotSupported;
+    const cuuint64_t dims[2] = {256, units}, strides[1] = {2048};
+    const cuuint32_t boxes[2] = {256, box}, steps[2] = {1, 1};
+    return fn(m, CU_TENSOR_MAP_DATA_TYPE_INT64, 2, const_cast<void*>(base), dims, strides, boxes, steps,
+              CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_NONE, CU_TENSOR_MAP_L2_PROMOTION_L2_256B,
+              CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS
                ? cudaSuccess
                : cudaErrorInvalidValue;
 }
@@ -718,22 +761,24 @@ W8Plan w8_plan_dense(int M, int NT, int G, int num_ctas) {
 
 cudaError_t launch_gemm_w8a8(W8Args a, const W8Operands& op, const W8Plan& plan, int num_ctas, cudaStream_t stream) {
     CUtensorMap mw, mx, ms;
-    cudaError_t e = make_map(&mw, op.wblocks, 128, (uint64_t)op.matrices * a.NT * a.G * kTileRows, 128, kTileRows, false);
+    cudaError_t e = make_map_linear(&mw, op.wblocks, (uint64_t)op.matrices * a.NT * a.G * (kTileRows / 16), kTileRows / 16);
     if (e != cudaSuccess) return e;
     a.BN = plan.bn;
     a.box_rows = plan.bn / plan.cg;  // 16 .. 128, a multiple of 16
     a.small_rows = 16;
     if (a.mt_tab != nullptr) {
-        // tiled rows [G][rows][128]
+        // tiled rows [G][rows][128]: a tile's rows of a plane lie together
         a.plane_x = 0;
-        a.plane_y = op.x_rows;
-        e = make_map(&mx, op.x, 128, (uint64_t)op.x_rows * a.G, 128, (uint32_t)a.box_rows, false);
-        if (e == cudaSuccess) e = make_map(&ms, op.x, 128, (uint64_t)op.x_rows * a.G, 128, (uint32_t)a.small_rows, false);
+        a.plane_y = op.x_rows / 16;
+        a.row_unit = 16;
+        e = make_map_linear(&mx, op.x, (uint64_t)op.x_rows / 16 * a.G, (uint32_t)a.box_rows / 16);
+        if (e == cudaSuccess) e = make_map_linear(&ms, op.x, (uint64_t)op.x_rows / 16 * a.G, (uint32_t)a.small_rows / 16);
     } else {
         // row-major rows of G * 128 bytes
         a.plane_x = 128;
         a.plane_y = 0;
-        e = make_map(&mx, op.x, (uint64_t)a.G * 128, (uint64_t)op.x_rows, (uint64_t)a.G * 128, (uint32_t)a.box_rows, true);
+        a.row_unit = 1;
+        e = make_map_rows(&mx, op.x, (uint64_t)a.G * 128, (uint64_t)op.x_rows, (uint32_t)a.box_rows);
         ms = mx;
         a.small_rows = 0;  // (rows past M are not read: the box costs what it holds)
     }

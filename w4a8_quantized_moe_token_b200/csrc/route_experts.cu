@@ -192,6 +192,7 @@ struct Row {
 // than the registers of one)
 template <typename T, int kPL, bool kVec>
 __global__ void __launch_bounds__(kRouteWarps * 32, kPL <= 12 ? 12 : kPL <= 16 ? 8 : 4) route_experts_kernel(const RouteArgs a) {
+    grid_dep_launch();
     grid_dep_wait();
     extern __shared__ double sm_choice[];
     const int lane = threadIdx.x & 31;

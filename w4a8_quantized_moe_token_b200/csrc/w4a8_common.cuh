@@ -365,6 +365,11 @@ __device__ __forceinline__ bool named_bar_or(int id, int nthreads, bool pred) {
 // ---------------------------------------------------------------------------
 __device__ __forceinline__ void grid_dep_wait() { asm volatile("griddepcontrol.wait;" ::: "memory"); }
 
+// Lets the next kernel of the stream start its set-up once every CTA of this grid has come
+// here.  A kernel that allocates tensor memory calls it only after its allocation: a later
+// kernel, which waits for this one, must not be able to take the columns first.
+__device__ __forceinline__ void grid_dep_launch() { asm volatile("griddepcontrol.launch_dependents;" ::: "memory"); }
+
 template <typename... KArgs, typename... Args>
 inline cudaError_t launch_pdl(void (*kernel)(KArgs...), dim3 grid, dim3 block, size_t smem, cudaStream_t stream,
                               Args... args) {

@@ -49,7 +49,8 @@ struct W8Args {
     int ns;                   // shared-memory stages
     uint32_t b_stage, recv;   // bytes of a stage's token block and of the K split's receive buffer
     int box_rows, small_rows; // token rows of the tile's tensor-map box and of the small one (0: none)
-    int plane_x, plane_y;     // tensor-map coordinates of K plane g: (g * plane_x, row + g * plane_y)
+    // tensor-map coordinates of token row r in K plane g: (g * plane_x, r / row_unit + g * plane_y)
+    int plane_x, plane_y, row_unit;
 };
 
 // What the tensor maps are built from.
