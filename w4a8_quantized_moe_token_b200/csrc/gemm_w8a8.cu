@@ -111,10 +111,11 @@ __device__ __forceinline__ uint32_t cluster_size() {
 }
 __device__ __forceinline__ void cluster_arrive() { asm volatile("barrier.cluster.arrive.release;" ::: "memory"); }
 __device__ __forceinline__ void cluster_wait() { asm volatile("barrier.cluster.wait.acquire;" ::: "memory"); }
-// store into another CTA's shared memory, reported to that CTA's barrier as 4 bytes
-__device__ __forceinline__ void st_async(uint32_t cluster_addr, uint32_t v, uint32_t cluster_bar) {
-    asm volatile("st.async.shared::cluster.mbarrier::complete_tx::bytes.b32 [%0], %1, [%2];" ::"r"(cluster_addr), "r"(v),
-                 "r"(cluster_bar)
+// 16 bytes into another CTA's shared memory, reported to that CTA's barrier as such
+__device__ __forceinline__ void st_async4(uint32_t cluster_addr, uint32_t x, uint32_t y, uint32_t z, uint32_t w,
+                                          uint32_t cluster_bar) {
+    asm volatile("st.async.shared::cluster.mbarrier::complete_tx::bytes.v4.b32 [%0], {%1, %2, %3, %4}, [%5];" ::"r"(cluster_addr),
+                 "r"(x), "r"(y), "r"(z), "r"(w), "r"(cluster_bar)
                  : "memory");
 }
 __device__ __forceinline__ void cluster_sync() {
@@ -193,6 +194,9 @@ __device__ __forceinline__ void w8_drain(uint32_t bar, uint32_t parity, long lon
         if (clock64() - t0 > limit) return;
 }
 
+// tokens of a tile that each CTA of a K split finishes
+__host__ __device__ inline int w8_tokens_per_part(int nrows, int parts) { return round_up(ceil_div(nrows, parts), 4); }
+
 struct W8Tile {
     int e, nt, row0, nrows;  // nt: weight tile of this CTA
 };
@@ -203,7 +207,7 @@ struct W8Tile {
 // which stay in L2 together whatever M and N are.
 template <int CG>
 __device__ __forceinline__ W8Tile w8_tile(int u, const W8Args& a, uint32_t rank) {
-    const int NP = (a.NT + CG - 1) / CG;
+    const int NP = a.NP;
     W8Tile t;
     if (a.mt_tab != nullptr) {
         const int mt = u / NP;
@@ -214,9 +218,8 @@ __device__ __forceinline__ W8Tile w8_tile(int u, const W8Args& a, uint32_t rank)
         t.nrows = v.z;
     } else {
         constexpr int kBlk = 8;
-        const int nmt = ceil_div(a.M, a.BN);
         const int g = u / (kBlk * NP), i = u - g * kBlk * NP;
-        const int size = min(kBlk, nmt - g * kBlk);
+        const int size = min(kBlk, a.nmt - g * kBlk);
         const int mt = g * kBlk + i % size;
         t.e = 0;
         t.nt = i / size * CG + (int)rank;
@@ -228,8 +231,64 @@ __device__ __forceinline__ W8Tile w8_tile(int u, const W8Args& a, uint32_t rank)
 
 __device__ __forceinline__ float w8_silu_mul(float g, float u) { return __fdividef(g, 1.0f + __expf(-g)) * u; }
 
-__device__ __forceinline__ uint16_t to_bits16(float v, int type) {
-    return type == W8A8_F16 ? __half_as_ushort(__float2half_rn(v)) : bf16_bits(v);
+// Output kinds of the epilogue.  kOutPair: 16-bit rows that may be stored two columns at a time.
+enum { kOutF32, kOutI32, kOutBf16, kOutF16, kOutPairBf16, kOutPairF16, kOutSwiglu };
+
+template <int kOut>
+__device__ __forceinline__ uint16_t to_bits16(float v) {
+    return kOut == kOutF16 || kOut == kOutPairF16 ? __half_as_ushort(__float2half_rn(v)) : bf16_bits(v);
+}
+
+// One chunk of 32 tokens of this lane's channel: v[i] is token i's INT32 sum, lane i holds
+// its scale sa.  `out`: this lane's element of the chunk's first row (kOutPair: column n - odd
+// of row `odd`; SwiGLU: column f of row `odd`), `pitch` bytes per row.  kFull: all 32 tokens
+// exist, else ncol of them.
+template <int kOut, bool kFull>
+__device__ __forceinline__ void w8_store_chunk(const uint32_t (&v)[32], float sw, float bias, float sa, int ncol, bool valid,
+                                               int odd, char* out, size_t pitch) {
+    if (kOut == kOutF32 || kOut == kOutI32 || kOut == kOutBf16 || kOut == kOutF16) {
+#pragma unroll
+        for (int i = 0; i < 32; ++i, out += pitch) {
+            const float y = kOut == kOutI32 ? 0.f : __int2float_rn((int)v[i]) * (sw * __shfl_sync(0xffffffffu, sa, i)) + bias;
+            if (valid && (kFull || i < ncol)) {
+                if (kOut == kOutF32) *reinterpret_cast<float*>(out) = y;
+                else if (kOut == kOutI32) *reinterpret_cast<uint32_t*>(out) = v[i];
+                else *reinterpret_cast<uint16_t*>(out) = to_bits16<kOut>(y);
+            }
+        }
+    } else if (kOut != kOutSwiglu) {
+        // the lanes of a pair swap one value per pair of tokens: the even lane stores two
+        // channels of token i, the odd lane of token i + 1
+#pragma unroll
+        for (int i = 0; i < 32; i += 2, out += 2 * pitch) {
+            const float p0 = __int2float_rn((int)v[i]) * (sw * __shfl_sync(0xffffffffu, sa, i)) + bias;
+            const float p1 = __int2float_rn((int)v[i + 1]) * (sw * __shfl_sync(0xffffffffu, sa, i + 1)) + bias;
+            const float recv = __shfl_xor_sync(0xffffffffu, odd ? p0 : p1, 1);
+            const uint32_t lo = to_bits16<kOut>(odd ? recv : p0), hi = to_bits16<kOut>(odd ? p1 : recv);
+            if (valid && (kFull || i + odd < ncol)) *reinterpret_cast<uint32_t*>(out) = lo | (hi << 16);
+        }
+    } else {
+        // even tile rows hold gate channel f, odd rows the matching up channel: per pair of
+        // tokens the lanes of a pair swap one value, the even lane finishes token i, the odd
+        // lane token i + 1
+#pragma unroll
+        for (int i = 0; i < 32; i += 2, out += 2 * pitch) {
+            const float p0 = __int2float_rn((int)v[i]) * sw, p1 = __int2float_rn((int)v[i + 1]) * sw;
+            const float recv = __shfl_xor_sync(0xffffffffu, odd ? p0 : p1, 1);
+            const float si = __shfl_sync(0xffffffffu, sa, i + odd);
+            const float gate = (odd ? recv : p0) * si, up = (odd ? p1 : recv) * si;
+            if (valid && (kFull || i + odd < ncol)) *reinterpret_cast<uint16_t*>(out) = bf16_bits(w8_silu_mul(gate, up));
+        }
+    }
+}
+
+template <int kOut>
+__device__ __forceinline__ void w8_store(const uint32_t (&v)[32], float sw, float bias, float sa, int ncol, bool valid, int odd,
+                                         char* out, size_t pitch) {
+    if (ncol == 32)
+        w8_store_chunk<kOut, true>(v, sw, bias, sa, ncol, valid, odd, out, pitch);
+    else
+        w8_store_chunk<kOut, false>(v, sw, bias, sa, ncol, valid, odd, out, pitch);
 }
 
 // kSplit (CG = 1, dense): the CTAs of a cluster share one tile, each taking a part of its K
@@ -284,7 +343,7 @@ __global__ void __launch_bounds__(kW8Threads, 1)
 
     grid_dep_launch();
     grid_dep_wait();  // the previous kernel on the stream has completed
-    const int total = ceil_div(a.NT, CG) * (a.mt_tab != nullptr ? __ldg(a.n_mtiles) : ceil_div(a.M, a.BN));
+    const int total = a.NP * (a.mt_tab != nullptr ? __ldg(a.n_mtiles) : a.nmt);
     // this CTA's K planes [g0, g1) of a tile; kSplit: one tile per cluster
     const int g0 = kSplit ? (int)((long long)a.G * part / parts) : 0;
     const int g1 = kSplit ? (int)((long long)a.G * (part + 1) / parts) : a.G;
@@ -378,14 +437,14 @@ __global__ void __launch_bounds__(kW8Threads, 1)
             const uint32_t b = tile & 1u;
             const float sw = t.nt < a.NT ? __ldg(a.wscale + ((size_t)t.e * a.NT + t.nt) * kTileRows + r) : 0.f;
             // output column: channel n (past the last tile: none valid)
-            const int n = a.mode == kW8Up ? t.nt * (kTileRows / 2) + (r >> 1) : t.nt * kTileRows + r;
+            const int n = a.out_kind == kOutSwiglu ? t.nt * (kTileRows / 2) + (r >> 1) : t.nt * kTileRows + r;
             const float bias = (a.bias != nullptr && n < a.nvalid) ? __ldg(a.bias + n) : 0.f;
             // token scales, ahead of the accumulator: kSplit, those of this CTA's tokens in shared
             // memory; otherwise lane l's of each chunk of 32 tokens in a register
             float* sa_s = reinterpret_cast<float*>(smem + (recv_full + 16 - base));
             float sa_r[CG * 2];
             if (kSplit) {
-                const int tok = (int)part * ceil_div(t.nrows, (int)parts) + (int)threadIdx.x;
+                const int tok = (int)part * w8_tokens_per_part(t.nrows, (int)parts) + (int)threadIdx.x;
                 if (threadIdx.x < 64) sa_s[threadIdx.x] = a.act_scale != nullptr && tok < t.nrows ? __ldg(a.act_scale + t.row0 + tok) : 0.f;
                 named_bar_sync(1, kW8EpiWarps * 32);
             } else {
@@ -398,49 +457,46 @@ __global__ void __launch_bounds__(kW8Threads, 1)
             if (!w8_wait(dfull + 8 * b, (tile >> 1) & 1u, abort_flag, a.err, a.wait_limit)) break;
             tc_fence_after();
             if (kSplit) {
-                // tokens [p * per, (p + 1) * per) are finished by CTA p, which keeps the
-                // partials of source s at recv[s][token][channel]
-                const int per = ceil_div(t.nrows, (int)parts);
+                // Tokens [p * per, (p + 1) * per) are finished by CTA p, which keeps the partials
+                // of source s at recv[s][token / 4][channel][token % 4]: a lane sends four tokens
+                // of its channel at a time, a warp 512 bytes in a row.
+                const int per = w8_tokens_per_part(t.nrows, (int)parts);
                 const int first = (int)part * per, count = max(0, min(per, t.nrows - first));
-                if (threadIdx.x == 0) mbar_arrive_expect_tx(recv_full, parts * (uint32_t)count * (kTileRows * 4u));
+                if (threadIdx.x == 0) mbar_arrive_expect_tx(recv_full, parts * (uint32_t)round_up(count, 4) * (kTileRows * 4u));
                 for (int c0 = half * 32; c0 < t.nrows; c0 += 64) {
                     uint32_t v[32];
                     tmem_ld32(tmem + ((uint32_t)(q * 32) << 16) + (uint32_t)c0, v);
                     tmem_ld_wait();
-                    int p = c0 / per, left = (p + 1) * per - c0;  // tokens left for CTA p
-                    uint32_t dst = mapa(recv, (uint32_t)p) + (uint32_t)(((int)part * per + c0 - p * per) * kTileRows + r) * 4u;
-                    uint32_t bar = mapa(recv_full, (uint32_t)p);
+                    int p = c0 / per, i0 = c0 - p * per;  // CTA and its token of the next four
 #pragma unroll
-                    for (int i = 0; i < 32; ++i) {
+                    for (int i = 0; i < 32; i += 4) {
                         if (c0 + i < t.nrows) {
-                            if (left == 0) {
-                                ++p;
-                                left = per;
-                                dst = mapa(recv, (uint32_t)p) + (uint32_t)((int)part * per * kTileRows + r) * 4u;
-                                bar = mapa(recv_full, (uint32_t)p);
-                            }
-                            st_async(dst, v[i], bar);
-                            dst += kTileRows * 4;
-                            --left;
+                            if (i0 == per) { ++p; i0 = 0; }
+                            st_async4(mapa(recv, (uint32_t)p) + (uint32_t)((((int)part * per + i0) / 4 * kTileRows + r) * 16), v[i],
+                                      v[i + 1], v[i + 2], v[i + 3], mapa(recv_full, (uint32_t)p));
+                            i0 += 4;
                         }
                     }
                 }
                 if (!w8_wait<true>(recv_full, 0, abort_flag, a.err, a.wait_limit)) break;
-                const int32_t* rb = reinterpret_cast<const int32_t*>(smem + (recv - base)) + r;
-                for (int i = half; i < count; i += 2) {
-                    int sum = 0;
-                    for (uint32_t src = 0; src < parts; ++src) sum += rb[((int)src * per + i) * kTileRows];
-                    const float sa = sa_s[i];
-                    const size_t at = (size_t)(t.row0 + first + i) * a.ldo + n;
-                    if (n < a.nvalid) {
-                        if (a.out_type == W8A8_I32) {
-                            static_cast<int32_t*>(a.out)[at] = sum;
-                        } else {
-                            const float y = __int2float_rn(sum) * (sw * sa) + bias;
-                            if (a.out_type == W8A8_F32)
-                                static_cast<float*>(a.out)[at] = y;
-                            else
-                                static_cast<uint16_t*>(a.out)[at] = to_bits16(y, a.out_type);
+                const int4* rb = reinterpret_cast<const int4*>(smem + (recv - base)) + r;
+                for (int i = half * 4; i < count; i += 8) {
+                    int4 sum = make_int4(0, 0, 0, 0);
+                    for (uint32_t src = 0; src < parts; ++src) {
+                        const int4 x = rb[((int)src * per + i) / 4 * kTileRows];
+                        sum.x += x.x; sum.y += x.y; sum.z += x.z; sum.w += x.w;
+                    }
+                    const int sums[4] = {sum.x, sum.y, sum.z, sum.w};
+#pragma unroll
+                    for (int k = 0; k < 4; ++k) {
+                        const size_t at = (size_t)(t.row0 + first + i + k) * a.ldo + n;
+                        if (n < a.nvalid && i + k < count) {
+                            const float y = __int2float_rn(sums[k]) * (sw * sa_s[i + k]) + bias;
+                            if (a.out_kind == kOutI32) static_cast<int32_t*>(a.out)[at] = sums[k];
+                            else if (a.out_kind == kOutF32) static_cast<float*>(a.out)[at] = y;
+                            else if (a.out_kind == kOutF16 || a.out_kind == kOutPairF16)
+                                static_cast<uint16_t*>(a.out)[at] = to_bits16<kOutF16>(y);
+                            else static_cast<uint16_t*>(a.out)[at] = to_bits16<kOutBf16>(y);
                         }
                     }
                 }
@@ -455,53 +511,20 @@ __global__ void __launch_bounds__(kW8Threads, 1)
                 uint32_t v[32];
                 tmem_ld32(tmem + ((uint32_t)(q * 32) << 16) + b * kAccCols + (uint32_t)c0, v);
                 tmem_ld_wait();
-                const size_t row = (size_t)(t.row0 + c0);
-                if (a.mode == kW8Up) {
-                    // even tile rows hold gate channel f, odd rows the matching up channel: per
-                    // pair of tokens (i, i+1) the lanes of a pair swap one value, the even lane
-                    // finishes token i, the odd lane token i+1
-                    uint16_t* h = static_cast<uint16_t*>(a.out) + (row + odd) * a.ldo + n;
-#pragma unroll
-                    for (int i = 0; i < 32; i += 2) {
-                        const float p0 = __int2float_rn((int)v[i]) * sw, p1 = __int2float_rn((int)v[i + 1]) * sw;
-                        const float recv = __shfl_xor_sync(0xffffffffu, odd ? p0 : p1, 1);
-                        const float si = __shfl_sync(0xffffffffu, sa, i + odd);
-                        const float gate = (odd ? recv : p0) * si, up = (odd ? p1 : recv) * si;
-                        if (n < a.nvalid && i + odd < ncol) h[(size_t)i * a.ldo] = bf16_bits(w8_silu_mul(gate, up));
-                    }
-                } else if (a.out_type == W8A8_F32) {
-                    float* y = static_cast<float*>(a.out) + row * a.ldo + n;
-#pragma unroll
-                    for (int i = 0; i < 32; ++i) {
-                        const float si = __shfl_sync(0xffffffffu, sa, i);
-                        if (n < a.nvalid && i < ncol) y[(size_t)i * a.ldo] = __int2float_rn((int)v[i]) * (sw * si) + bias;
-                    }
-                } else if (a.out_type == W8A8_I32) {
-                    int32_t* y = static_cast<int32_t*>(a.out) + row * a.ldo + n;
-#pragma unroll
-                    for (int i = 0; i < 32; ++i)
-                        if (n < a.nvalid && i < ncol) y[(size_t)i * a.ldo] = (int32_t)v[i];
-                } else if (a.pairs) {
-                    // two channels per store: the lanes of a pair swap one value per pair of
-                    // tokens, the even lane stores token i, the odd lane token i+1
-                    uint16_t* y = static_cast<uint16_t*>(a.out) + (row + odd) * a.ldo + (n - odd);
-#pragma unroll
-                    for (int i = 0; i < 32; i += 2) {
-                        const float p0 = __int2float_rn((int)v[i]) * (sw * __shfl_sync(0xffffffffu, sa, i)) + bias;
-                        const float p1 = __int2float_rn((int)v[i + 1]) * (sw * __shfl_sync(0xffffffffu, sa, i + 1)) + bias;
-                        const float recv = __shfl_xor_sync(0xffffffffu, odd ? p0 : p1, 1);
-                        const uint32_t lo = to_bits16(odd ? recv : p0, a.out_type), hi = to_bits16(odd ? p1 : recv, a.out_type);
-                        if (n < a.nvalid && i + odd < ncol)
-                            *reinterpret_cast<uint32_t*>(y + (size_t)i * a.ldo) = lo | (hi << 16);
-                    }
-                } else {
-                    uint16_t* y = static_cast<uint16_t*>(a.out) + row * a.ldo + n;
-#pragma unroll
-                    for (int i = 0; i < 32; ++i) {
-                        const float si = __shfl_sync(0xffffffffu, sa, i);
-                        if (n < a.nvalid && i < ncol)
-                            y[(size_t)i * a.ldo] = to_bits16(__int2float_rn((int)v[i]) * (sw * si) + bias, a.out_type);
-                    }
+                const int el = a.out_kind == kOutF32 || a.out_kind == kOutI32 ? 4 : 2;
+                const bool pair = a.out_kind == kOutPairBf16 || a.out_kind == kOutPairF16;
+                const size_t pitch = (size_t)a.ldo * el;
+                const int row = t.row0 + c0 + (pair || a.out_kind == kOutSwiglu ? odd : 0);
+                char* out = static_cast<char*>(a.out) + (size_t)row * pitch + (size_t)(n - (pair ? odd : 0)) * el;
+                const bool valid = n < a.nvalid;
+                switch (a.out_kind) {
+                    case kOutF32: w8_store<kOutF32>(v, sw, bias, sa, ncol, valid, odd, out, pitch); break;
+                    case kOutI32: w8_store<kOutI32>(v, sw, bias, sa, ncol, valid, odd, out, pitch); break;
+                    case kOutBf16: w8_store<kOutBf16>(v, sw, bias, sa, ncol, valid, odd, out, pitch); break;
+                    case kOutF16: w8_store<kOutF16>(v, sw, bias, sa, ncol, valid, odd, out, pitch); break;
+                    case kOutPairBf16: w8_store<kOutPairBf16>(v, sw, bias, sa, ncol, valid, odd, out, pitch); break;
+                    case kOutPairF16: w8_store<kOutPairF16>(v, sw, bias, sa, ncol, valid, odd, out, pitch); break;
+                    default: w8_store<kOutSwiglu>(v, sw, bias, sa, ncol, valid, odd, out, pitch); break;
                 }
             }
             tc_fence_before();
@@ -731,10 +754,12 @@ W8Plan w8_plan_grouped(int avg_tokens) {
     return {2, round_up(ceil_div(want, tiles), 32), 1};
 }
 
-// The cheapest of the tile shapes by a model of a tile's time in cycles: per K plane the
-// tensor core's 2 * bn or the arrival of its blocks (128 + bn / cg rows of 128 bytes at
-// about 40 bytes per cycle and SM), whichever is longer, plus the fill of the pipeline and
-// the epilogue, plus the exchange of a K split.
+// The cheapest of the tile shapes by a model of the kernel's time in cycles, fitted to
+// measurements on B200: about 6200 (a pair: 7850) from launch to end for one step; per K
+// plane the tensor core's 2 * bn or the arrival of its blocks (128 + bn / cg rows of 128
+// bytes at 57 bytes per cycle and SM; a pair: 48), and not less than 480; the last tile's
+// epilogue; the exchange of a K split.  At 4096 x 4096, 64 rows: 11.7 us unsplit, 7.9 us in
+// four parts; 128 rows: 13.4 and 9.9 us.
 W8Plan w8_plan_dense(int M, int NT, int G, int num_ctas) {
     W8Plan best = {1, 128, 1};
     long long best_cost = -1;
@@ -742,17 +767,18 @@ W8Plan w8_plan_dense(int M, int NT, int G, int num_ctas) {
         const long long tiles = (long long)ceil_div(M, bn) * ceil_div(NT, cg);
         const long long slots = num_ctas / (cg * split);
         if (slots < 1 || split > G || (split > 1 && tiles > slots)) return;
-        const int rows = 128 + bn / cg;
-        const long long plane = 2 * bn > rows * 16 / 5 ? 2 * bn : rows * 16 / 5;
+        const long long arrival = cg == 1 ? (128 + bn) * 9 / 4 : (128 + bn / 2) * 53 / 20;
+        const long long mma = 2 * bn > 480 ? 2 * bn : 480;
         const long long waves = (tiles + slots - 1) / slots;
-        const long long cost = waves * (ceil_div(G, split) * plane + 500) + 2500 + 8 * bn + (split > 1 ? 1200 + 8 * bn : 0);
+        const long long cost = waves * (ceil_div(G, split) * (arrival > mma ? arrival : mma) + 300) + (cg == 1 ? 6200 : 7850) +
+                               13 * bn + (split > 1 ? 600 + 56 * bn : 0);
         if (best_cost < 0 || cost < best_cost) {
             best_cost = cost;
             best = {cg, bn, split};
         }
     };
     const int top = M < 128 ? round_up(M, 16) : 128;
-    for (int bn = top; bn >= 16; bn = bn > 16 && bn < 32 ? 16 : bn / 32 * 16)
+    for (int bn = top; bn >= 16; bn -= 16)
         for (int split = 1; split <= 8; split *= 2) consider(1, bn, split);
     if (M > 64)
         for (int bn = 256; bn >= 64; bn -= 32) consider(2, bn, 1);
@@ -764,6 +790,8 @@ cudaError_t launch_gemm_w8a8(W8Args a, const W8Operands& op, const W8Plan& plan,
     cudaError_t e = make_map_linear(&mw, op.wblocks, (uint64_t)op.matrices * a.NT * a.G * (kTileRows / 16), kTileRows / 16);
     if (e != cudaSuccess) return e;
     a.BN = plan.bn;
+    a.NP = ceil_div(a.NT, plan.cg);
+    a.nmt = ceil_div(a.M, plan.bn);
     a.box_rows = plan.bn / plan.cg;  // 16 .. 128, a multiple of 16
     a.small_rows = 16;
     if (a.mt_tab != nullptr) {
@@ -783,9 +811,14 @@ cudaError_t launch_gemm_w8a8(W8Args a, const W8Operands& op, const W8Plan& plan,
         a.small_rows = 0;  // (rows past M are not read: the box costs what it holds)
     }
     if (e != cudaSuccess) return e;
-    a.pairs = a.ldo % 2 == 0 && reinterpret_cast<uintptr_t>(a.out) % 4 == 0;
+    const bool pairs = a.ldo % 2 == 0 && reinterpret_cast<uintptr_t>(a.out) % 4 == 0;
+    a.out_kind = a.mode == kW8Up            ? kOutSwiglu
+                 : a.out_type == W8A8_F32   ? kOutF32
+                 : a.out_type == W8A8_I32   ? kOutI32
+                 : a.out_type == W8A8_BF16  ? (pairs ? kOutPairBf16 : kOutBf16)
+                                            : (pairs ? kOutPairF16 : kOutF16);
     a.b_stage = (uint32_t)a.box_rows * 128u;
-    a.recv = plan.split > 1 ? (uint32_t)(ceil_div(plan.bn, plan.split) * plan.split * kTileRows * 4) : 0u;
+    a.recv = plan.split > 1 ? (uint32_t)(w8_tokens_per_part(plan.bn, plan.split) * plan.split * kTileRows * 4) : 0u;
     a.ns = (kW8SmemMax - kW8BarBytes - (int)a.recv) / (kW8BlockBytes + (int)a.b_stage);
     if (a.ns > kW8MaxStages) a.ns = kW8MaxStages;
     const int steps = ceil_div(a.G, plan.split);  // a short K needs no more stages

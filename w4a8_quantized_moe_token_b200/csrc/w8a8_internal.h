@@ -45,7 +45,8 @@ struct W8Args {
     long long wait_limit;     // clock cycles a bounded wait may last
     uint32_t debug;           // test hook
     // set by the launcher
-    int pairs;                // 16-bit rows may be stored two columns at a time
+    int out_kind;             // the epilogue's variant
+    int NP, nmt;              // weight tiles (of cg * 128 channels) per matrix; dense: row tiles
     int ns;                   // shared-memory stages
     uint32_t b_stage, recv;   // bytes of a stage's token block and of the K split's receive buffer
     int box_rows, small_rows; // token rows of the tile's tensor-map box and of the small one (0: none)
