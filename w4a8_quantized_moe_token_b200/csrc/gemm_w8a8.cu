@@ -43,8 +43,9 @@ constexpr int kW8MmaWarp = kW8ProdWarp + kW8Producers;
 constexpr int kW8Threads = 32 * (kW8MmaWarp + 1);
 constexpr int kW8MaxStages = 12;
 // shared memory: ns weight blocks, ns token blocks (both 1024-aligned: swizzle atoms), the
-// receive buffer of a K split, barriers (full, empty, 2 x accumulator full / empty, receive)
-constexpr int kW8BarBytes = (2 * kW8MaxStages + 5) * 8 + 16 + 64 * 4;  // + the K split's token scales
+// receive buffer of a K split, barriers (full, empty, 2 x accumulator full / empty, receive),
+// token scales
+constexpr int kW8BarBytes = (2 * kW8MaxStages + 5) * 8 + 16 + kW8EpiWarps * 32 * 4;  // + token scales
 constexpr int kW8SmemMax = 227 * 1024 - 1024;  // without the alignment slack
 inline int w8_smem(int ns, int b_stage, int recv) { return ns * (kW8BlockBytes + b_stage) + recv + kW8BarBytes + 1024; }
 
@@ -239,51 +240,57 @@ __device__ __forceinline__ uint16_t to_bits16(float v) {
     return kOut == kOutF16 || kOut == kOutPairF16 ? __half_as_ushort(__float2half_rn(v)) : bf16_bits(v);
 }
 
-// One chunk of 32 tokens of this lane's channel: v[i] is token i's INT32 sum, lane i holds
-// its scale sa.  `out`: this lane's element of the chunk's first row (kOutPair: column n - odd
-// of row `odd`; SwiGLU: column f of row `odd`), `pitch` bytes per row.  kFull: all 32 tokens
-// exist, else ncol of them.
+// One chunk of 32 tokens of this lane's channel: v[i] is token i's INT32 sum, sa[i] its scale
+// (shared memory).  `out`: this lane's element of the chunk's first row (kOutPair: column
+// n - odd of row `odd`; SwiGLU: column f of row `odd`), `pitch` bytes per row.  kFull: all 32
+// tokens exist, else ncol of them.
 template <int kOut, bool kFull>
-__device__ __forceinline__ void w8_store_chunk(const uint32_t (&v)[32], float sw, float bias, float sa, int ncol, bool valid,
-                                               int odd, char* out, size_t pitch) {
-    if (kOut == kOutF32 || kOut == kOutI32 || kOut == kOutBf16 || kOut == kOutF16) {
+__device__ __forceinline__ void w8_store_chunk(const uint32_t (&v)[32], float sw, float bias, const float* sa, int ncol,
+                                               bool valid, int odd, char* out, size_t pitch) {
 #pragma unroll
-        for (int i = 0; i < 32; ++i, out += pitch) {
-            const float y = kOut == kOutI32 ? 0.f : __int2float_rn((int)v[i]) * (sw * __shfl_sync(0xffffffffu, sa, i)) + bias;
-            if (valid && (kFull || i < ncol)) {
-                if (kOut == kOutF32) *reinterpret_cast<float*>(out) = y;
-                else if (kOut == kOutI32) *reinterpret_cast<uint32_t*>(out) = v[i];
-                else *reinterpret_cast<uint16_t*>(out) = to_bits16<kOut>(y);
+    for (int i4 = 0; i4 < 32; i4 += 4) {
+        const float4 s4 = *reinterpret_cast<const float4*>(sa + i4);
+        const float s[4] = {s4.x, s4.y, s4.z, s4.w};
+        if (kOut == kOutF32 || kOut == kOutI32 || kOut == kOutBf16 || kOut == kOutF16) {
+#pragma unroll
+            for (int k = 0; k < 4; ++k, out += pitch) {
+                const float y = kOut == kOutI32 ? 0.f : __int2float_rn((int)v[i4 + k]) * (sw * s[k]) + bias;
+                if (valid && (kFull || i4 + k < ncol)) {
+                    if (kOut == kOutF32) *reinterpret_cast<float*>(out) = y;
+                    else if (kOut == kOutI32) *reinterpret_cast<uint32_t*>(out) = v[i4 + k];
+                    else *reinterpret_cast<uint16_t*>(out) = to_bits16<kOut>(y);
+                }
             }
-        }
-    } else if (kOut != kOutSwiglu) {
-        // the lanes of a pair swap one value per pair of tokens: the even lane stores two
-        // channels of token i, the odd lane of token i + 1
+        } else if (kOut != kOutSwiglu) {
+            // the lanes of a pair swap one value per pair of tokens: the even lane stores two
+            // channels of token i, the odd lane of token i + 1
 #pragma unroll
-        for (int i = 0; i < 32; i += 2, out += 2 * pitch) {
-            const float p0 = __int2float_rn((int)v[i]) * (sw * __shfl_sync(0xffffffffu, sa, i)) + bias;
-            const float p1 = __int2float_rn((int)v[i + 1]) * (sw * __shfl_sync(0xffffffffu, sa, i + 1)) + bias;
-            const float recv = __shfl_xor_sync(0xffffffffu, odd ? p0 : p1, 1);
-            const uint32_t lo = to_bits16<kOut>(odd ? recv : p0), hi = to_bits16<kOut>(odd ? p1 : recv);
-            if (valid && (kFull || i + odd < ncol)) *reinterpret_cast<uint32_t*>(out) = lo | (hi << 16);
-        }
-    } else {
-        // even tile rows hold gate channel f, odd rows the matching up channel: per pair of
-        // tokens the lanes of a pair swap one value, the even lane finishes token i, the odd
-        // lane token i + 1
+            for (int k = 0; k < 4; k += 2, out += 2 * pitch) {
+                const float p0 = __int2float_rn((int)v[i4 + k]) * (sw * s[k]) + bias;
+                const float p1 = __int2float_rn((int)v[i4 + k + 1]) * (sw * s[k + 1]) + bias;
+                const float recv = __shfl_xor_sync(0xffffffffu, odd ? p0 : p1, 1);
+                const uint32_t lo = to_bits16<kOut>(odd ? recv : p0), hi = to_bits16<kOut>(odd ? p1 : recv);
+                if (valid && (kFull || i4 + k + odd < ncol)) *reinterpret_cast<uint32_t*>(out) = lo | (hi << 16);
+            }
+        } else {
+            // even tile rows hold gate channel f, odd rows the matching up channel: per pair
+            // of tokens the lanes of a pair swap one value, the even lane finishes token i,
+            // the odd lane token i + 1
 #pragma unroll
-        for (int i = 0; i < 32; i += 2, out += 2 * pitch) {
-            const float p0 = __int2float_rn((int)v[i]) * sw, p1 = __int2float_rn((int)v[i + 1]) * sw;
-            const float recv = __shfl_xor_sync(0xffffffffu, odd ? p0 : p1, 1);
-            const float si = __shfl_sync(0xffffffffu, sa, i + odd);
-            const float gate = (odd ? recv : p0) * si, up = (odd ? p1 : recv) * si;
-            if (valid && (kFull || i + odd < ncol)) *reinterpret_cast<uint16_t*>(out) = bf16_bits(w8_silu_mul(gate, up));
+            for (int k = 0; k < 4; k += 2, out += 2 * pitch) {
+                const float p0 = __int2float_rn((int)v[i4 + k]) * sw, p1 = __int2float_rn((int)v[i4 + k + 1]) * sw;
+                const float recv = __shfl_xor_sync(0xffffffffu, odd ? p0 : p1, 1);
+                const float si = odd ? s[k + 1] : s[k];
+                const float gate = (odd ? recv : p0) * si, up = (odd ? p1 : recv) * si;
+                if (valid && (kFull || i4 + k + odd < ncol))
+                    *reinterpret_cast<uint16_t*>(out) = bf16_bits(w8_silu_mul(gate, up));
+            }
         }
     }
 }
 
 template <int kOut>
-__device__ __forceinline__ void w8_store(const uint32_t (&v)[32], float sw, float bias, float sa, int ncol, bool valid, int odd,
+__device__ __forceinline__ void w8_store(const uint32_t (&v)[32], float sw, float bias, const float* sa, int ncol, bool valid, int odd,
                                          char* out, size_t pitch) {
     if (ncol == 32)
         w8_store_chunk<kOut, true>(v, sw, bias, sa, ncol, valid, odd, out, pitch);
@@ -439,14 +446,14 @@ __global__ void __launch_bounds__(kW8Threads, 1)
             // output column: channel n (past the last tile: none valid)
             const int n = a.out_kind == kOutSwiglu ? t.nt * (kTileRows / 2) + (r >> 1) : t.nt * kTileRows + r;
             const float bias = (a.bias != nullptr && n < a.nvalid) ? __ldg(a.bias + n) : 0.f;
-            // token scales, ahead of the accumulator: kSplit, those of this CTA's tokens in shared
-            // memory; otherwise lane l's of each chunk of 32 tokens in a register
+            // token scales, ahead of the accumulator: lane l's of each chunk of 32 tokens in a
+            // register (kSplit: those of this CTA's tokens in shared memory)
             float* sa_s = reinterpret_cast<float*>(smem + (recv_full + 16 - base));
             float sa_r[CG * 2];
             if (kSplit) {
                 const int tok = (int)part * w8_tokens_per_part(t.nrows, (int)parts) + (int)threadIdx.x;
                 if (threadIdx.x < 64) sa_s[threadIdx.x] = a.act_scale != nullptr && tok < t.nrows ? __ldg(a.act_scale + t.row0 + tok) : 0.f;
-                named_bar_sync(1, kW8EpiWarps * 32);
+                named_bar_sync(1, kW8EpiWarps * 32);  // (one tile: every epilogue warp comes here once)
             } else {
 #pragma unroll
                 for (int c = 0; c < CG * 2; ++c) {
@@ -507,9 +514,12 @@ __global__ void __launch_bounds__(kW8Threads, 1)
                 const int c0 = half * 32 + c * 64;
                 if (c0 >= t.nrows) break;
                 const int ncol = min(32, t.nrows - c0);  // tokens of this chunk
-                const float sa = sa_r[c];
                 uint32_t v[32];
                 tmem_ld32(tmem + ((uint32_t)(q * 32) << 16) + b * kAccCols + (uint32_t)c0, v);
+                float* sa_w = sa_s + warp * 32;  // this warp's own 32 (eight broadcast reads for a shuffle per token)
+                __syncwarp();
+                sa_w[lane] = sa_r[c];
+                __syncwarp();
                 tmem_ld_wait();
                 const int el = a.out_kind == kOutF32 || a.out_kind == kOutI32 ? 4 : 2;
                 const bool pair = a.out_kind == kOutPairBf16 || a.out_kind == kOutPairF16;
@@ -518,13 +528,13 @@ __global__ void __launch_bounds__(kW8Threads, 1)
                 char* out = static_cast<char*>(a.out) + (size_t)row * pitch + (size_t)(n - (pair ? odd : 0)) * el;
                 const bool valid = n < a.nvalid;
                 switch (a.out_kind) {
-                    case kOutF32: w8_store<kOutF32>(v, sw, bias, sa, ncol, valid, odd, out, pitch); break;
-                    case kOutI32: w8_store<kOutI32>(v, sw, bias, sa, ncol, valid, odd, out, pitch); break;
-                    case kOutBf16: w8_store<kOutBf16>(v, sw, bias, sa, ncol, valid, odd, out, pitch); break;
-                    case kOutF16: w8_store<kOutF16>(v, sw, bias, sa, ncol, valid, odd, out, pitch); break;
-                    case kOutPairBf16: w8_store<kOutPairBf16>(v, sw, bias, sa, ncol, valid, odd, out, pitch); break;
-                    case kOutPairF16: w8_store<kOutPairF16>(v, sw, bias, sa, ncol, valid, odd, out, pitch); break;
-                    default: w8_store<kOutSwiglu>(v, sw, bias, sa, ncol, valid, odd, out, pitch); break;
+                    case kOutF32: w8_store<kOutF32>(v, sw, bias, sa_w, ncol, valid, odd, out, pitch); break;
+                    case kOutI32: w8_store<kOutI32>(v, sw, bias, sa_w, ncol, valid, odd, out, pitch); break;
+                    case kOutBf16: w8_store<kOutBf16>(v, sw, bias, sa_w, ncol, valid, odd, out, pitch); break;
+                    case kOutF16: w8_store<kOutF16>(v, sw, bias, sa_w, ncol, valid, odd, out, pitch); break;
+                    case kOutPairBf16: w8_store<kOutPairBf16>(v, sw, bias, sa_w, ncol, valid, odd, out, pitch); break;
+                    case kOutPairF16: w8_store<kOutPairF16>(v, sw, bias, sa_w, ncol, valid, odd, out, pitch); break;
+                    default: w8_store<kOutSwiglu>(v, sw, bias, sa_w, ncol, valid, odd, out, pitch); break;
                 }
             }
             tc_fence_before();
@@ -700,20 +710,60 @@ cudaError_t make_map_linear(CUtensorMap* m, const void* base, uint64_t units, ui
 
 namespace {
 
+// Per device, looked up once: the instances' shared-memory attribute is set, and how many
+// clusters of 2, 4 and 8 CTAs run at once with one CTA per SM (clusters stay inside a GPC,
+// whose SMs need not be a multiple of the cluster).
+struct W8Device {
+    int pairs = 0;         // CG = 2
+    int clusters[4] = {};  // K split by 1 << i (index 0 unused)
+};
+
 template <int CG, bool kSplit>
-cudaError_t launch_instance(const CUtensorMap& mw, const CUtensorMap& mx, const CUtensorMap& ms, const W8Args& a, int smem, int grid, int cluster,
-                            cudaStream_t stream) {
+cudaError_t max_clusters(int cluster, int* n) {
     const auto kernel = gemm_w8a8_kernel<CG, kSplit>;
+    cudaError_t e = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, 227 * 1024);
+    if (e != cudaSuccess || cluster == 1) return e;
+    cudaLaunchConfig_t cfg = {};
+    cfg.gridDim = (unsigned)cluster;
+    cfg.blockDim = kW8Threads;
+    cfg.dynamicSmemBytes = 227 * 1024;
+    cudaLaunchAttribute attr;
+    attr.id = cudaLaunchAttributeClusterDimension;
+    attr.val.clusterDim.x = (unsigned)cluster;
+    attr.val.clusterDim.y = attr.val.clusterDim.z = 1;
+    cfg.attrs = &attr;
+    cfg.numAttrs = 1;
+    return cudaOccupancyMaxActiveClusters(n, kernel, &cfg);
+}
+
+cudaError_t w8_device(W8Device* out) {
     static std::mutex mu;
-    static int clusters[64] = {0};  // per device: pairs that fit at once (CG = 2), 1 once prepared
+    static W8Device devs[64];
     int dev = 0;
     cudaError_t e = cudaGetDevice(&dev);
     if (e != cudaSuccess) return e;
     if (dev < 0 || dev >= 64) return cudaErrorInvalidDevice;
+    std::lock_guard<std::mutex> lock(mu);
+    if (devs[dev].pairs == 0) {
+        W8Device d;
+        e = max_clusters<1, false>(1, nullptr);
+        for (int i = 1; e == cudaSuccess && i <= 3; ++i) e = max_clusters<1, true>(1 << i, &d.clusters[i]);
+        if (e == cudaSuccess) e = max_clusters<2, false>(2, &d.pairs);
+        if (e != cudaSuccess) return e;
+        if (d.pairs < 1) return cudaErrorInvalidConfiguration;
+        devs[dev] = d;
+    }
+    *out = devs[dev];
+    return cudaSuccess;
+}
+
+template <int CG, bool kSplit>
+cudaError_t launch_instance(const CUtensorMap& mw, const CUtensorMap& mx, const CUtensorMap& ms, const W8Args& a, int smem, int grid,
+                            int cluster, cudaStream_t stream) {
     cudaLaunchConfig_t cfg = {};
-    cfg.gridDim = grid;
+    cfg.gridDim = (unsigned)grid;
     cfg.blockDim = kW8Threads;
-    cfg.dynamicSmemBytes = smem;
+    cfg.dynamicSmemBytes = (size_t)smem;
     cfg.stream = stream;
     cudaLaunchAttribute attr[2];
     attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
@@ -723,49 +773,20 @@ cudaError_t launch_instance(const CUtensorMap& mw, const CUtensorMap& mx, const 
     attr[1].val.clusterDim.y = attr[1].val.clusterDim.z = 1;
     cfg.attrs = attr;
     cfg.numAttrs = cluster == 1 ? 1 : 2;
-    {
-        std::lock_guard<std::mutex> lock(mu);
-        if (clusters[dev] == 0) {
-            e = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, 227 * 1024);
-            if (e != cudaSuccess) return e;
-            int n = 1;
-            if (CG == 2) {
-                cudaLaunchConfig_t q = cfg;
-                q.dynamicSmemBytes = 227 * 1024;
-                q.attrs = attr + 1;
-                q.numAttrs = 1;
-                e = cudaOccupancyMaxActiveClusters(&n, kernel, &q);
-                if (e != cudaSuccess) return e;
-                if (n < 1) return cudaErrorInvalidConfiguration;
-            }
-            clusters[dev] = n;
-        }
-        if (CG == 2 && grid > clusters[dev] * CG) cfg.gridDim = clusters[dev] * CG;
-    }
-    return cudaLaunchKernelEx(&cfg, kernel, mw, mx, ms, a);
+    return cudaLaunchKernelEx(&cfg, gemm_w8a8_kernel<CG, kSplit>, mw, mx, ms, a);
 }
 
-}  // namespace
-
-W8Plan w8_plan_grouped(int avg_tokens) {
-    if (avg_tokens < 64) return {1, 128, 1};
-    const int want = avg_tokens + avg_tokens / 10;  // most experts' rows in equal tiles
-    const int tiles = ceil_div(want, 256);
-    return {2, round_up(ceil_div(want, tiles), 32), 1};
-}
-
-// The cheapest of the tile shapes by a model of the kernel's time in cycles, fitted to
+// The cheapest of the dense tile shapes by a model of the kernel's time in cycles, fitted to
 // measurements on B200: about 6200 (a pair: 7850) from launch to end for one step; per K
 // plane the tensor core's 2 * bn or the arrival of its blocks (128 + bn / cg rows of 128
 // bytes at 57 bytes per cycle and SM; a pair: 48), and not less than 480; the last tile's
 // epilogue; the exchange of a K split.  At 4096 x 4096, 64 rows: 11.7 us unsplit, 7.9 us in
 // four parts; 128 rows: 13.4 and 9.9 us.
-W8Plan w8_plan_dense(int M, int NT, int G, int num_ctas) {
+W8Plan w8_plan_dense(int M, int NT, int G, int num_ctas, const W8Device& dev) {
     W8Plan best = {1, 128, 1};
     long long best_cost = -1;
-    const auto consider = [&](int cg, int bn, int split) {
+    const auto consider = [&](int cg, int bn, int split, int slots) {
         const long long tiles = (long long)ceil_div(M, bn) * ceil_div(NT, cg);
-        const long long slots = num_ctas / (cg * split);
         if (slots < 1 || split > G || (split > 1 && tiles > slots)) return;
         const long long arrival = cg == 1 ? (128 + bn) * 9 / 4 : (128 + bn / 2) * 53 / 20;
         const long long mma = 2 * bn > 480 ? 2 * bn : 480;
@@ -778,16 +799,67 @@ W8Plan w8_plan_dense(int M, int NT, int G, int num_ctas) {
         }
     };
     const int top = M < 128 ? round_up(M, 16) : 128;
-    for (int bn = top; bn >= 16; bn -= 16)
-        for (int split = 1; split <= 8; split *= 2) consider(1, bn, split);
+    for (int bn = top; bn >= 16; bn -= 16) {
+        consider(1, bn, 1, num_ctas);
+        for (int i = 1; i <= 3; ++i) consider(1, bn, 1 << i, dev.clusters[i]);
+    }
     if (M > 64)
-        for (int bn = 256; bn >= 64; bn -= 32) consider(2, bn, 1);
+        for (int bn = 256; bn >= 64; bn -= 32) consider(2, bn, 1, dev.pairs);
     return best;
 }
 
-cudaError_t launch_gemm_w8a8(W8Args a, const W8Operands& op, const W8Plan& plan, int num_ctas, cudaStream_t stream) {
+}  // namespace
+
+// The grouped tile shape by the same model, for nslots rows spread evenly over the experts: a
+// step's blocks come from L2 as above, but its weight block at least once per expert from
+// memory (16 KB per CTA at 6.5 TB/s for all SMs: 700 cycles).  B200, up + down projections of
+// 48 experts (H 4096, F 1408): 85 rows each, 170 us with 128 x 128 tiles, 176 us with pairs;
+// 170 rows each (H 7168, F 2048): 558 against 405 us.
+W8Plan w8_plan_grouped(int nslots, int E, int NT_up, int G_up, int NT_down, int G_down, int num_ctas) {
+    const int experts = nslots < E ? nslots : E;
+    const int rows = ceil_div(nslots, experts);
+    const auto cost = [&](int cg, int bn) {
+        const int mt = ceil_div(rows, bn), r = ceil_div(rows, mt);  // row tiles per expert, rows of one
+        const long long slots = num_ctas / cg, memory = 700 / mt;
+        long long plane = cg == 1 ? (128 + r) * 9 / 4 : (128 + r / 2) * 53 / 20;
+        plane = plane > 480 ? plane : 480;
+        plane = plane > memory ? plane : memory;
+        plane = plane > 2 * r ? plane : 2 * r;
+        long long sum = 0;
+        for (int down = 0; down < 2; ++down) {
+            const long long tiles = (long long)experts * mt * ceil_div(down ? NT_down : NT_up, cg);
+            const long long loop = (down ? G_down : G_up) * plane;
+            const long long epilogue = 16ll * r;  // overlaps the next tile's loop
+            sum += (tiles + slots - 1) / slots * (loop > epilogue ? loop : epilogue) + epilogue + (cg == 1 ? 6200 : 7850);
+        }
+        return sum;
+    };
+    // (rows vary: tiles a tenth wider than the mean's equal shares)
+    const int want = rows + rows / 10;
+    W8Plan best = {1, 128, 1};
+    long long best_cost = rows < 64 ? 0 : cost(1, 128);
+    const auto consider = [&](int cg, int bn) {
+        const long long c = cost(cg, bn);
+        if (c < best_cost) {
+            best_cost = c;
+            best = {cg, bn, 1};
+        }
+    };
+    consider(1, 64);
+    for (int mt = ceil_div(want, 256); mt <= ceil_div(want, 128) + 1; ++mt) {
+        const int bn = round_up(ceil_div(want, mt), 32);
+        consider(2, bn < 64 ? 64 : bn);
+    }
+    return best;
+}
+
+cudaError_t launch_gemm_w8a8(W8Args a, const W8Operands& op, const W8Plan* grouped, int num_ctas, cudaStream_t stream) {
+    W8Device dev;
+    cudaError_t e = w8_device(&dev);
+    if (e != cudaSuccess) return e;
+    const W8Plan plan = grouped != nullptr ? *grouped : w8_plan_dense(a.M, a.NT, a.G, num_ctas, dev);
     CUtensorMap mw, mx, ms;
-    cudaError_t e = make_map_linear(&mw, op.wblocks, (uint64_t)op.matrices * a.NT * a.G * (kTileRows / 16), kTileRows / 16);
+    e = make_map_linear(&mw, op.wblocks, (uint64_t)op.matrices * a.NT * a.G * (kTileRows / 16), kTileRows / 16);
     if (e != cudaSuccess) return e;
     a.BN = plan.bn;
     a.NP = ceil_div(a.NT, plan.cg);
@@ -830,7 +902,8 @@ cudaError_t launch_gemm_w8a8(W8Args a, const W8Operands& op, const W8Plan& plan,
         return launch_instance<1, true>(mw, mx, ms, a, smem, grid, plan.split, stream);
     }
     if (plan.cg == 1) return launch_instance<1, false>(mw, mx, ms, a, smem, num_ctas, 1, stream);
-    return launch_instance<2, false>(mw, mx, ms, a, smem, num_ctas / 2 * 2, 2, stream);
+    const int at_once = num_ctas / 2 < dev.pairs ? num_ctas / 2 : dev.pairs;
+    return launch_instance<2, false>(mw, mx, ms, a, smem, at_once * 2, 2, stream);
 }
 
 cudaError_t launch_pack_w8(const uint16_t* w, int E, int N, int K, int layout, uint8_t* packed, int8_t* codes, float* scale,

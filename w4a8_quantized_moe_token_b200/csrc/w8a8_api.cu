@@ -112,8 +112,7 @@ W4A8_EXPORT int w8a8_gemm(const int8_t* qa, const float* sa, int M, const void* 
     op.x = qa;
     op.x_rows = M;
     ProfScope prof(W4A8_KERNEL_GEMM_DENSE, 1, s);
-    const int sms = sm_count();
-    W8_TRY(launch_gemm_w8a8(a, op, w8_plan_dense(M, a.NT, a.G, sms), sms, s));
+    W8_TRY(launch_gemm_w8a8(a, op, nullptr, sm_count(), s));
     return W4A8_OK;
 }
 
@@ -166,7 +165,8 @@ W4A8_EXPORT int w8a8_moe_forward(const void* packed_up, const void* packed_down,
     float* s2 = at<float>(ws, L, R_S2);
     uint16_t* h = at<uint16_t>(ws, L, R_H);
     float* y2 = at<float>(ws, L, R_Y2);
-    const W8Plan plan = w8_plan_grouped(L.nslots / E);
+    const W8Plan plan = w8_plan_grouped(L.nslots, E, w8_tiles(2 * F, W4A8_LAYOUT_GATEUP), L.G1, w8_tiles(H, W4A8_LAYOUT_PLAIN), L.G2,
+                                        sm_count());
     {
         ProfScope p(W4A8_KERNEL_PERM, perm_launch_count(L.nslots), st);
         W8_TRY(launch_perm(ids, L.nslots, E, plan.bn, at<int>(ws, L, R_CHIST), L.nchunk, at<int>(ws, L, R_COUNTS), offs, poffs,
@@ -198,7 +198,7 @@ W4A8_EXPORT int w8a8_moe_forward(const void* packed_up, const void* packed_down,
     op.x_rows = L.R;
     {
         ProfScope p(W4A8_KERNEL_GEMM_UP, 1, st);
-        W8_TRY(launch_gemm_w8a8(a, op, plan, sm_count(), st));
+        W8_TRY(launch_gemm_w8a8(a, op, &plan, sm_count(), st));
     }
     {
         ProfScope p(W4A8_KERNEL_REQUANT, 1, st);
@@ -217,7 +217,7 @@ W4A8_EXPORT int w8a8_moe_forward(const void* packed_up, const void* packed_down,
     op.x = act2;
     {
         ProfScope p(W4A8_KERNEL_GEMM_DOWN, 1, st);
-        W8_TRY(launch_gemm_w8a8(a, op, plan, sm_count(), st));
+        W8_TRY(launch_gemm_w8a8(a, op, &plan, sm_count(), st));
     }
     {
         ProfScope p(W4A8_KERNEL_COMBINE, 1, st);

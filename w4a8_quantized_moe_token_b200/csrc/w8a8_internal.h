@@ -68,12 +68,11 @@ struct W8Plan {
     int cg, bn, split;
 };
 
-// the tile shape for a dense layer of M rows, NT weight tiles and G K planes on num_ctas SMs
-W8Plan w8_plan_dense(int M, int NT, int G, int num_ctas);
-// ... for a grouped layer with this mean number of tokens per expert; the permutation's
-// row-tile table must be built with bn
-W8Plan w8_plan_grouped(int avg_tokens);
-cudaError_t launch_gemm_w8a8(W8Args a, const W8Operands& op, const W8Plan& plan, int num_ctas, cudaStream_t stream);
+// the tile shape for both projections of nslots rows over E experts (weight tiles and K planes
+// of each); the permutation's row-tile table must be built with bn
+W8Plan w8_plan_grouped(int nslots, int E, int NT_up, int G_up, int NT_down, int G_down, int num_ctas);
+// grouped: the plan of the row-tile table; dense (null): the launcher chooses
+cudaError_t launch_gemm_w8a8(W8Args a, const W8Operands& op, const W8Plan* grouped, int num_ctas, cudaStream_t stream);
 cudaError_t launch_pack_w8(const uint16_t* w, int E, int N, int K, int layout, uint8_t* packed, int8_t* codes, float* scale,
                            cudaStream_t stream);
 
