@@ -240,6 +240,15 @@ __device__ __forceinline__ uint16_t to_bits16(float v) {
     return kOut == kOutF16 || kOut == kOutPairF16 ? __half_as_ushort(__float2half_rn(v)) : bf16_bits(v);
 }
 
+// predicated stores: a branch around each would keep the values' arithmetic from overlapping
+// (SwiGLU tiles of 16 K planes 41 against 37 us)
+__device__ __forceinline__ void st_if(bool p, void* at, uint32_t v) {
+    asm volatile("{\n\t.reg .pred p;\n\tsetp.ne.b32 p, %2, 0;\n\t@p st.global.b32 [%0], %1;\n\t}" ::"l"(at), "r"(v), "r"((int)p) : "memory");
+}
+__device__ __forceinline__ void st_if(bool p, void* at, uint16_t v) {
+    asm volatile("{\n\t.reg .pred p;\n\tsetp.ne.b32 p, %2, 0;\n\t@p st.global.b16 [%0], %1;\n\t}" ::"l"(at), "h"(v), "r"((int)p) : "memory");
+}
+
 // One chunk of 32 tokens of this lane's channel: v[i] is token i's INT32 sum, sa[i] its scale
 // (shared memory).  `out`: this lane's element of the chunk's first row (kOutPair: column
 // n - odd of row `odd`; SwiGLU: column f of row `odd`), `pitch` bytes per row.  kFull: all 32
@@ -255,11 +264,10 @@ __device__ __forceinline__ void w8_store_chunk(const uint32_t (&v)[32], float sw
 #pragma unroll
             for (int k = 0; k < 4; ++k, out += pitch) {
                 const float y = kOut == kOutI32 ? 0.f : __int2float_rn((int)v[i4 + k]) * (sw * s[k]) + bias;
-                if (valid && (kFull || i4 + k < ncol)) {
-                    if (kOut == kOutF32) *reinterpret_cast<float*>(out) = y;
-                    else if (kOut == kOutI32) *reinterpret_cast<uint32_t*>(out) = v[i4 + k];
-                    else *reinterpret_cast<uint16_t*>(out) = to_bits16<kOut>(y);
-                }
+                const bool p = valid && (kFull || i4 + k < ncol);
+                if (kOut == kOutF32) st_if(p, out, __float_as_uint(y));
+                else if (kOut == kOutI32) st_if(p, out, v[i4 + k]);
+                else st_if(p, out, to_bits16<kOut>(y));
             }
         } else if (kOut != kOutSwiglu) {
             // the lanes of a pair swap one value per pair of tokens: the even lane stores two
@@ -270,7 +278,7 @@ __device__ __forceinline__ void w8_store_chunk(const uint32_t (&v)[32], float sw
                 const float p1 = __int2float_rn((int)v[i4 + k + 1]) * (sw * s[k + 1]) + bias;
                 const float recv = __shfl_xor_sync(0xffffffffu, odd ? p0 : p1, 1);
                 const uint32_t lo = to_bits16<kOut>(odd ? recv : p0), hi = to_bits16<kOut>(odd ? p1 : recv);
-                if (valid && (kFull || i4 + k + odd < ncol)) *reinterpret_cast<uint32_t*>(out) = lo | (hi << 16);
+                st_if(valid && (kFull || i4 + k + odd < ncol), out, lo | (hi << 16));
             }
         } else {
             // even tile rows hold gate channel f, odd rows the matching up channel: per pair
@@ -282,8 +290,7 @@ __device__ __forceinline__ void w8_store_chunk(const uint32_t (&v)[32], float sw
                 const float recv = __shfl_xor_sync(0xffffffffu, odd ? p0 : p1, 1);
                 const float si = odd ? s[k + 1] : s[k];
                 const float gate = (odd ? recv : p0) * si, up = (odd ? p1 : recv) * si;
-                if (valid && (kFull || i4 + k + odd < ncol))
-                    *reinterpret_cast<uint16_t*>(out) = bf16_bits(w8_silu_mul(gate, up));
+                st_if(valid && (kFull || i4 + k + odd < ncol), out, bf16_bits(w8_silu_mul(gate, up)));
             }
         }
     }

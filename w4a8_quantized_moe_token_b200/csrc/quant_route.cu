@@ -643,6 +643,7 @@ __global__ void __launch_bounds__(128) act_scatter_kernel(const uint16_t* __rest
                                                           const int* __restrict__ offs,
                                                           const int* __restrict__ poffs, int RB,
                                                           int8_t* __restrict__ act, float* __restrict__ s) {
+    if (kW8) grid_dep_launch();
     grid_dep_wait();  // the previous kernel of the forward has completed
     const int nch = Kp / 16;
     const int G = Kp / kGroup;
@@ -720,6 +721,7 @@ template <int kCache, bool kW8>
 __global__ void __launch_bounds__(128) requant_kernel(const uint16_t* __restrict__ h, int ldh, int F, int Kp,
                                                       const int* __restrict__ row_src, const int* __restrict__ poffs,
                                                       int E, int RB, int8_t* __restrict__ act, float* __restrict__ s) {
+    if (kW8) grid_dep_launch();
     grid_dep_wait();  // the previous kernel of the forward has completed
     const int r = blockIdx.x;
     if (r >= __ldg(poffs + E)) return;
@@ -727,11 +729,176 @@ __global__ void __launch_bounds__(128) requant_kernel(const uint16_t* __restrict
 }
 
 // ---------------------------------------------------------------------------
+// W8A8 layer, up to kPrepareSlots slots: the permutation and the activation quantisation in
+// one kernel.  CTA t quantises token t; every CTA counts all ids for itself (a few thousand
+// integers from L2, cheaper than a kernel of its own in front: 8 us of the one-token layer's
+// chain), and a slot's place among its expert's rows is the number of earlier slots with the
+// same id, so the grouping is that of the permutation kernels.  CTA 0 writes the tables and
+// the error word.  Pad rows are not written: nothing that depends on them is ever read.
+// ---------------------------------------------------------------------------
+// exclusive scan over 256 threads
+__device__ __forceinline__ int scan256(int v, int* sh, int* total) {
+    const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
+    int incl = v;
+#pragma unroll
+    for (int o = 1; o < 32; o <<= 1) {
+        const int n = __shfl_up_sync(0xffffffffu, incl, o);
+        if (lane >= o) incl += n;
+    }
+    __syncthreads();
+    if (lane == 31) sh[warp] = incl;
+    __syncthreads();
+    int before = 0, all = 0;
+#pragma unroll
+    for (int w = 0; w < 8; ++w) {
+        if (w < warp) before += sh[w];
+        all += sh[w];
+    }
+    *total = all;
+    return before + incl - v;
+}
+
+__global__ void __launch_bounds__(256) w8_prepare_kernel(const int32_t* __restrict__ ids, const uint16_t* __restrict__ x,
+                                                         int T, int H, int Kp, int k, int E, int tile_tokens,
+                                                         int* __restrict__ counts, int* __restrict__ offs,
+                                                         int* __restrict__ poffs, int* __restrict__ mtstart,
+                                                         int4* __restrict__ mt_tab, int* __restrict__ perm,
+                                                         int* __restrict__ inv, int* __restrict__ row_src, int RB,
+                                                         int8_t* __restrict__ act, float* __restrict__ s,
+                                                         uint32_t* __restrict__ err) {
+    grid_dep_launch();
+    grid_dep_wait();
+    __shared__ int s_ids[kPrepareSlots];
+    __shared__ int s_off[kMaxExperts], s_poff[kMaxExperts];  // counts first, then offsets
+    __shared__ int sh[8], dst[32], s_bad;
+    __shared__ float red[8];
+    const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
+    const int tok = blockIdx.x, nslots = T * k;
+    const int nch = Kp / 16, G = Kp / kGroup;
+    const uint16_t* row = x + (size_t)tok * H;
+    // the token's row: up to two chunks per thread in registers, loading while the ids are counted
+    Chunk16 cache[2];
+#pragma unroll
+    for (int c = 0; c < 2; ++c)
+        if (tid + c * 256 < nch) load_chunk(row, H, (tid + c * 256) * 16, cache[c]);
+    if (tid == 0) s_bad = 0;
+    for (int e = tid; e < E; e += 256) s_off[e] = 0;
+    __syncthreads();
+    for (int i = tid; i < nslots; i += 256) {
+        const int e = __ldg(ids + i);
+        const bool good = e >= 0 && e < E;
+        s_ids[i] = good ? e : -1;
+        if (good) atomicAdd(&s_off[e], 1);
+        else s_bad = 1;
+    }
+    __syncthreads();
+    // thread t scans experts 4t .. 4t + 3
+    int c4[4], o = 0, p = 0, m = 0;
+#pragma unroll
+    for (int i = 0; i < 4; ++i) {
+        c4[i] = 4 * tid + i < E ? s_off[4 * tid + i] : 0;
+        o += c4[i];
+        p += round_up(c4[i], kRowPad);
+        m += ceil_div(c4[i], tile_tokens);
+    }
+    int ot, pt, mt;
+    o = scan256(o, sh, &ot);
+    p = scan256(p, sh, &pt);
+    if (tok == 0) m = scan256(m, sh, &mt);
+#pragma unroll
+    for (int i = 0; i < 4; ++i) {
+        const int e = 4 * tid + i;
+        if (e < E) {
+            if (tok == 0) {
+                counts[e] = c4[i];
+                offs[e] = o;
+                poffs[e] = p;
+                mtstart[e] = m;
+                for (int r = p + c4[i]; r < p + round_up(c4[i], kRowPad); ++r) row_src[r] = -1;
+                for (int q = 0; q < ceil_div(c4[i], tile_tokens); ++q)
+                    mt_tab[m + q] = make_int4(e, p + q * tile_tokens, min(tile_tokens, c4[i] - q * tile_tokens), 0);
+            }
+            s_off[e] = o;
+            s_poff[e] = p;
+            o += c4[i];
+            p += round_up(c4[i], kRowPad);
+            m += ceil_div(c4[i], tile_tokens);
+        }
+    }
+    if (tok == 0 && tid == 0) {
+        offs[E] = ot;
+        poffs[E] = pt;
+        mtstart[E] = mt;
+        *err = s_bad ? kErrBadExpert : 0u;
+    }
+    __syncthreads();
+    // a warp per slot of the token: how many earlier slots chose the same expert
+    for (int j = warp; j < k; j += 8) {
+        const int slot = tok * k + j, e = s_ids[slot];
+        int n = 0;
+        for (int i = lane; i < slot; i += 32) n += s_ids[i] == e;
+#pragma unroll
+        for (int w = 16; w > 0; w >>= 1) n += __shfl_xor_sync(0xffffffffu, n, w);
+        if (lane == 0) {
+            const int r = e >= 0 ? s_poff[e] + n : -1;
+            dst[j] = r;
+            inv[slot] = r;
+            if (e >= 0) {
+                perm[s_off[e] + n] = slot;
+                row_src[r] = slot;
+            }
+        }
+    }
+    // quantise the row and write it to its k places
+    float amax = 0.f;
+#pragma unroll
+    for (int c = 0; c < 2; ++c)
+        if (tid + c * 256 < nch) {
+#pragma unroll
+            for (int i = 0; i < 16; ++i) amax = fmaxf(amax, fabsf(cache[c].v[i]));
+        }
+    for (int ci = tid + 512; ci < nch; ci += 256) {
+        Chunk16 tmp;
+        load_chunk(row, H, ci * 16, tmp);
+#pragma unroll
+        for (int i = 0; i < 16; ++i) amax = fmaxf(amax, fabsf(tmp.v[i]));
+    }
+    amax = warp_max(amax);
+    if (lane == 0) red[warp] = amax;
+    __syncthreads();
+#pragma unroll
+    for (int w = 0; w < 8; ++w) amax = fmaxf(amax, red[w]);
+    const float sc = row_scale<true>(amax);
+    const float rinv = __fdiv_rn(1.0f, sc);
+    auto emit = [&](int ci, const Chunk16& c) {
+        uint32_t out[4] = {0u, 0u, 0u, 0u};
+        if (amax > 0.f) {
+#pragma unroll
+            for (int i = 0; i < 16; ++i) out[i >> 2] |= (uint32_t)(quant_i8_fast(c.v[i], sc, rinv) & 0xFF) << (8 * (i & 3));
+        }
+        const uint4 q = make_uint4(out[0], out[1], out[2], out[3]);
+        for (int j = 0; j < k; ++j)
+            if (dst[j] >= 0) *reinterpret_cast<uint4*>(act + act_offset(dst[j], ci * 16, G, RB)) = q;
+    };
+#pragma unroll
+    for (int c = 0; c < 2; ++c)
+        if (tid + c * 256 < nch) emit(tid + c * 256, cache[c]);
+    for (int ci = tid + 512; ci < nch; ci += 256) {
+        Chunk16 tmp;
+        load_chunk(row, H, ci * 16, tmp);
+        emit(ci, tmp);
+    }
+    if (tid < k && dst[tid] >= 0) s[dst[tid]] = sc;
+}
+
+// ---------------------------------------------------------------------------
 // a8: out[t] = sum_j w[t][j] * y2[inv[t*k+j]]  (fp32, j ascending) -> bf16
 // ---------------------------------------------------------------------------
+template <bool kW8>
 __global__ void __launch_bounds__(256) combine_kernel(const float* __restrict__ y2, int H, const int* __restrict__ inv,
                                                       const float* __restrict__ w, int T, int k,
                                                       uint16_t* __restrict__ out) {
+    if (kW8) grid_dep_launch();
     grid_dep_wait();  // the previous kernel of the forward has completed
     __shared__ int rows[32];
     __shared__ float wts[32];
@@ -928,6 +1095,13 @@ cudaError_t launch_act_scatter(const uint16_t* x, int T, int H, int Kp, int k, c
                       offs, poffs, rb, act, s);
 }
 
+cudaError_t launch_w8_prepare(const int32_t* ids, const uint16_t* x, int T, int H, int Kp, int k, int E, int tile_tokens,
+                              int* counts, int* offs, int* poffs, int* mtstart, int4* mt_tab, int* perm, int* inv, int* row_src,
+                              int rb, int8_t* act, float* s, uint32_t* err, cudaStream_t stream) {
+    return launch_pdl(w8_prepare_kernel, T, 256, 0, stream, ids, x, T, H, Kp, k, E, tile_tokens, counts, offs, poffs, mtstart,
+                      mt_tab, perm, inv, row_src, rb, act, s, err);
+}
+
 cudaError_t launch_requant(const uint16_t* h, int ldh, int F, int Kp, const int* row_src, const int* poffs, int E,
                            int rows_cap, int rb, int8_t* act, float* s, cudaStream_t stream, bool w8) {
     if (rows_cap == 0) return cudaSuccess;
@@ -937,9 +1111,9 @@ cudaError_t launch_requant(const uint16_t* h, int ldh, int F, int Kp, const int*
 }
 
 cudaError_t launch_combine(const float* y2, int H, const int* inv, const float* w, int T, int k, uint16_t* out,
-                           cudaStream_t stream) {
+                           cudaStream_t stream, bool w8) {
     if (T == 0) return cudaSuccess;
-    return launch_pdl(combine_kernel, T, 256, 0, stream, y2, H, inv, w, T, k, out);
+    return launch_pdl(w8 ? combine_kernel<true> : combine_kernel<false>, T, 256, 0, stream, y2, H, inv, w, T, k, out);
 }
 
 cudaError_t launch_dense_prep(const int8_t* qa, int M, int Kq, int Kp, int tile_tokens, int rb, int8_t* act, int4* mt_tab,

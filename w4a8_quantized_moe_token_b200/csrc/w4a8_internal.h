@@ -114,9 +114,15 @@ cudaError_t launch_act_scatter(const uint16_t* x, int T, int H, int Kp, int k, c
 // h: bf16 SwiGLU output rows of ldh values
 cudaError_t launch_requant(const uint16_t* h, int ldh, int F, int Kp, const int* row_src, const int* poffs, int E,
                            int rows_cap, int rb, int8_t* act, float* s, cudaStream_t stream, bool w8 = false);
+// W8A8 layer, T * k <= kPrepareSlots: launch_perm and launch_act_scatter (w8) in one kernel,
+// which also sets the error word
+constexpr int kPrepareSlots = 2048;
+cudaError_t launch_w8_prepare(const int32_t* ids, const uint16_t* x, int T, int H, int Kp, int k, int E, int tile_tokens,
+                              int* counts, int* offs, int* poffs, int* mtstart, int4* mt_tab, int* perm, int* inv, int* row_src,
+                              int rb, int8_t* act, float* s, uint32_t* err, cudaStream_t stream);
 // y2: fp32 expert outputs [rows][H]
 cudaError_t launch_combine(const float* y2, int H, const int* inv, const float* w, int T, int k, uint16_t* out,
-                           cudaStream_t stream);
+                           cudaStream_t stream, bool w8 = false);
 // qa rows of Kq columns into tiled rows of Kp >= Kq columns (the rest zero)
 cudaError_t launch_dense_prep(const int8_t* qa, int M, int Kq, int Kp, int tile_tokens, int rb, int8_t* act, int4* mt_tab,
                               int* n_mtiles, cudaStream_t stream);

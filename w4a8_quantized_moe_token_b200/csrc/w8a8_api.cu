@@ -152,7 +152,7 @@ W4A8_EXPORT int w8a8_moe_forward(const void* packed_up, const void* packed_down,
     }
     cudaStream_t st = static_cast<cudaStream_t>(stream);
     uint32_t* err = at<uint32_t>(ws, L, R_ERR);
-    W8_TRY(cudaMemsetAsync(err, 0, 16, st));
+    if (T == 0 || L.nslots > kPrepareSlots) W8_TRY(cudaMemsetAsync(err, 0, 16, st));
     if (T == 0) return W4A8_OK;
     int* offs = at<int>(ws, L, R_OFFS);
     int* poffs = at<int>(ws, L, R_POFFS);
@@ -167,14 +167,19 @@ W4A8_EXPORT int w8a8_moe_forward(const void* packed_up, const void* packed_down,
     float* y2 = at<float>(ws, L, R_Y2);
     const W8Plan plan = w8_plan_grouped(L.nslots, E, w8_tiles(2 * F, W4A8_LAYOUT_GATEUP), L.G1, w8_tiles(H, W4A8_LAYOUT_PLAIN), L.G2,
                                         sm_count());
-    {
-        ProfScope p(W4A8_KERNEL_PERM, perm_launch_count(L.nslots), st);
-        W8_TRY(launch_perm(ids, L.nslots, E, plan.bn, at<int>(ws, L, R_CHIST), L.nchunk, at<int>(ws, L, R_COUNTS), offs, poffs,
-                           mtstart, at<int4>(ws, L, R_MTTAB), at<int>(ws, L, R_PERM), inv, row_src, err, st));
-    }
-    {
+    const uint16_t* x = static_cast<const uint16_t*>(x_bf16);
+    if (L.nslots <= kPrepareSlots) {
         ProfScope p(W4A8_KERNEL_ACT_QUANT, 1, st);
-        W8_TRY(launch_act_scatter(static_cast<const uint16_t*>(x_bf16), T, H, L.Hp, k, inv, offs, poffs, E, L.R, act1, s1, st, true));
+        W8_TRY(launch_w8_prepare(ids, x, T, H, L.Hp, k, E, plan.bn, at<int>(ws, L, R_COUNTS), offs, poffs, mtstart,
+                                 at<int4>(ws, L, R_MTTAB), at<int>(ws, L, R_PERM), inv, row_src, L.R, act1, s1, err, st));
+    } else {
+        {
+            ProfScope p(W4A8_KERNEL_PERM, perm_launch_count(L.nslots), st);
+            W8_TRY(launch_perm(ids, L.nslots, E, plan.bn, at<int>(ws, L, R_CHIST), L.nchunk, at<int>(ws, L, R_COUNTS), offs,
+                               poffs, mtstart, at<int4>(ws, L, R_MTTAB), at<int>(ws, L, R_PERM), inv, row_src, err, st));
+        }
+        ProfScope p(W4A8_KERNEL_ACT_QUANT, 1, st);
+        W8_TRY(launch_act_scatter(x, T, H, L.Hp, k, inv, offs, poffs, E, L.R, act1, s1, st, true));
     }
     W8Args a{};
     W8Operands op{};
@@ -221,7 +226,7 @@ W4A8_EXPORT int w8a8_moe_forward(const void* packed_up, const void* packed_down,
     }
     {
         ProfScope p(W4A8_KERNEL_COMBINE, 1, st);
-        W8_TRY(launch_combine(y2, H, inv, w, T, k, static_cast<uint16_t*>(out_bf16), st));
+        W8_TRY(launch_combine(y2, H, inv, w, T, k, static_cast<uint16_t*>(out_bf16), st, true));
     }
     return W4A8_OK;
 }
