@@ -42,6 +42,9 @@ def test_packed_bytes(lib):
     assert lib.w8a8_packed_bytes(3, 100, 200, 0) == 256 + 3 * 512 + 3 * 2 * blk
     assert lib.w8a8_packed_bytes(8, 2048, 2048, 1) == 256 + 8 * 16 * 512 + 8 * 16 * 16 * blk
     assert lib.w8a8_packed_bytes(1, 66, 1, 1) == 256 + 512 + blk
+    for E, N, K in [(1, 256, 512), (3, 100, 200), (2, 2, 1)]:  # what the binding checks against
+        assert B._w8_packed_size(E, -(-N // 128), K) == lib.w8a8_packed_bytes(E, N, K, 0)
+        assert B._w8_packed_size(E, -(-(N // 2) // 64), K) == lib.w8a8_packed_bytes(E, N, K, 1)
     assert lib.w8a8_packed_bytes(1, 3, 128, 1) == 0   # odd N for gate|up
     assert lib.w8a8_packed_bytes(1, 4, 128, 2) == 0   # unknown layout
     assert lib.w8a8_packed_bytes(1, 4, 128, 0x100) == 0  # W4A8 scheme flags do not apply

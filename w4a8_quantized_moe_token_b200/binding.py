@@ -509,6 +509,11 @@ def w8a8_pack_weights(w: torch.Tensor, layout: int, packed: torch.Tensor, codes=
                                    _stream()), "w8a8_pack_weights")
 
 
+def _w8_packed_size(E: int, tiles: int, K: int) -> int:
+    """w8a8_packed_bytes of E matrices with this many 128-row tiles each (without a call)."""
+    return 256 + E * tiles * (512 + (K + 127) // 128 * 16384)
+
+
 def w8a8_gemm_workspace_bytes(M, N, K) -> int:
     return lib().w8a8_gemm_workspace_bytes(M, N, K)
 
@@ -536,7 +541,7 @@ def w8a8_gemm(qa, sa, packed, N, K, y, ws, bias=None):
         if bias.shape != (N,):
             raise W4A8Error(f"bias must be [N={N}], got {tuple(bias.shape)}")
     L = _lib or lib()
-    if packed.numel() < L.w8a8_packed_bytes(1, N, K, W4A8_LAYOUT_PLAIN):
+    if packed.numel() < _w8_packed_size(1, (N + 127) // 128, K):
         raise W4A8Error("packed is smaller than the packed weights of an N x K matrix")
     st = L.w8a8_gemm(_at(qa, torch.int8, "qa", dev), sa_at, M, _at(packed, torch.uint8, "packed", dev), N, K, bias_at,
                      _at(y, dtype, "y", dev), _OUT_TYPE[dtype], _at(ws, torch.uint8, "ws", dev), ws.numel(), _raw_stream(dev))
@@ -570,9 +575,9 @@ def w8a8_moe_forward(packed_up, packed_down, E, H, F, x, ids, w, out, ws):
     if out.shape != (T, H):
         raise W4A8Error(f"out must be [T={T}][H={H}], got {tuple(out.shape)}")
     L = _lib or lib()
-    if packed_up.numel() < L.w8a8_packed_bytes(E, 2 * F, H, W4A8_LAYOUT_GATEUP):
+    if packed_up.numel() < _w8_packed_size(E, (F + 63) // 64, H):
         raise W4A8Error("packed_up is smaller than the packed gate|up weights of this layer")
-    if packed_down.numel() < L.w8a8_packed_bytes(E, H, F, W4A8_LAYOUT_PLAIN):
+    if packed_down.numel() < _w8_packed_size(E, (H + 127) // 128, F):
         raise W4A8Error("packed_down is smaller than the packed down weights of this layer")
     st = L.w8a8_moe_forward(
         _at(packed_up, torch.uint8, "packed_up", dev), _at(packed_down, torch.uint8, "packed_down", dev), E, H, F,

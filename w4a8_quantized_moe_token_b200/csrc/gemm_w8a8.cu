@@ -249,60 +249,110 @@ __device__ __forceinline__ void st_if(bool p, void* at, uint16_t v) {
     asm volatile("{\n\t.reg .pred p;\n\tsetp.ne.b32 p, %2, 0;\n\t@p st.global.b16 [%0], %1;\n\t}" ::"l"(at), "h"(v), "r"((int)p) : "memory");
 }
 
-// One chunk of 32 tokens of this lane's channel: v[i] is token i's INT32 sum, sa[i] its scale
+// One chunk of 16 tokens of this lane's channel: v[i] is token i's INT32 sum, sa[i] its scale
 // (shared memory).  `out`: this lane's element of the chunk's first row (kOutPair: column
-// n - odd of row `odd`; SwiGLU: column f of row `odd`), `pitch` bytes per row.  kFull: all 32
-// tokens exist, else ncol of them.
-template <int kOut, bool kFull>
-__device__ __forceinline__ void w8_store_chunk(const uint32_t (&v)[32], float sw, float bias, const float* sa, int ncol,
-                                               bool valid, int odd, char* out, size_t pitch) {
+// n - odd of row `odd`; SwiGLU: column f of row `odd`), `pitch` bytes per row; the first ncol
+// tokens exist.  Short on purpose, and called in a loop that is not unrolled: with 32 tokens
+// and everything unrolled the epilogue waited for its instructions more than for anything
+// else.
+template <int kOut>
+__device__ __forceinline__ void w8_store(const uint32_t (&v)[16], float sw, float bias, const float* sa, int ncol, bool valid,
+                                         int odd, char* out, size_t pitch) {
+    float s[16];
 #pragma unroll
-    for (int i4 = 0; i4 < 32; i4 += 4) {
-        const float4 s4 = *reinterpret_cast<const float4*>(sa + i4);
-        const float s[4] = {s4.x, s4.y, s4.z, s4.w};
-        if (kOut == kOutF32 || kOut == kOutI32 || kOut == kOutBf16 || kOut == kOutF16) {
+    for (int i = 0; i < 16; i += 4) {
+        const float4 s4 = *reinterpret_cast<const float4*>(sa + i);
+        s[i] = s4.x; s[i + 1] = s4.y; s[i + 2] = s4.z; s[i + 3] = s4.w;
+    }
+    if (kOut == kOutF32 || kOut == kOutI32 || kOut == kOutBf16 || kOut == kOutF16) {
 #pragma unroll
-            for (int k = 0; k < 4; ++k, out += pitch) {
-                const float y = kOut == kOutI32 ? 0.f : __int2float_rn((int)v[i4 + k]) * (sw * s[k]) + bias;
-                const bool p = valid && (kFull || i4 + k < ncol);
-                if (kOut == kOutF32) st_if(p, out, __float_as_uint(y));
-                else if (kOut == kOutI32) st_if(p, out, v[i4 + k]);
-                else st_if(p, out, to_bits16<kOut>(y));
-            }
-        } else if (kOut != kOutSwiglu) {
-            // the lanes of a pair swap one value per pair of tokens: the even lane stores two
-            // channels of token i, the odd lane of token i + 1
-#pragma unroll
-            for (int k = 0; k < 4; k += 2, out += 2 * pitch) {
-                const float p0 = __int2float_rn((int)v[i4 + k]) * (sw * s[k]) + bias;
-                const float p1 = __int2float_rn((int)v[i4 + k + 1]) * (sw * s[k + 1]) + bias;
-                const float recv = __shfl_xor_sync(0xffffffffu, odd ? p0 : p1, 1);
-                const uint32_t lo = to_bits16<kOut>(odd ? recv : p0), hi = to_bits16<kOut>(odd ? p1 : recv);
-                st_if(valid && (kFull || i4 + k + odd < ncol), out, lo | (hi << 16));
-            }
-        } else {
-            // even tile rows hold gate channel f, odd rows the matching up channel: per pair
-            // of tokens the lanes of a pair swap one value, the even lane finishes token i,
-            // the odd lane token i + 1
-#pragma unroll
-            for (int k = 0; k < 4; k += 2, out += 2 * pitch) {
-                const float p0 = __int2float_rn((int)v[i4 + k]) * sw, p1 = __int2float_rn((int)v[i4 + k + 1]) * sw;
-                const float recv = __shfl_xor_sync(0xffffffffu, odd ? p0 : p1, 1);
-                const float si = odd ? s[k + 1] : s[k];
-                const float gate = (odd ? recv : p0) * si, up = (odd ? p1 : recv) * si;
-                st_if(valid && (kFull || i4 + k + odd < ncol), out, bf16_bits(w8_silu_mul(gate, up)));
-            }
+        for (int i = 0; i < 16; ++i, out += pitch) {
+            const float y = kOut == kOutI32 ? 0.f : __int2float_rn((int)v[i]) * (sw * s[i]) + bias;
+            const bool p = valid && i < ncol;
+            if (kOut == kOutF32) st_if(p, out, __float_as_uint(y));
+            else if (kOut == kOutI32) st_if(p, out, v[i]);
+            else st_if(p, out, to_bits16<kOut>(y));
         }
+    } else if (kOut != kOutSwiglu) {
+        // the lanes of a pair swap one value per pair of tokens: the even lane stores two
+        // channels of token i, the odd lane of token i + 1
+        float own[8], recv[8];
+#pragma unroll
+        for (int i = 0; i < 16; i += 2) {
+            const float p0 = __int2float_rn((int)v[i]) * (sw * s[i]) + bias;
+            const float p1 = __int2float_rn((int)v[i + 1]) * (sw * s[i + 1]) + bias;
+            own[i / 2] = odd ? p1 : p0;
+            recv[i / 2] = __shfl_xor_sync(0xffffffffu, odd ? p0 : p1, 1);
+        }
+#pragma unroll
+        for (int i = 0; i < 16; i += 2, out += 2 * pitch) {
+            const uint32_t lo = to_bits16<kOut>(odd ? recv[i / 2] : own[i / 2]), hi = to_bits16<kOut>(odd ? own[i / 2] : recv[i / 2]);
+            st_if(valid && i + odd < ncol, out, lo | (hi << 16));
+        }
+    } else {
+        // even tile rows hold gate channel f, odd rows the matching up channel: per pair of
+        // tokens the lanes of a pair swap one value, the even lane finishes token i, the odd
+        // lane token i + 1 (shuffles first, then arithmetic, then stores: the first and the
+        // last keep their order among themselves)
+        float own[8], recv[8];
+#pragma unroll
+        for (int i = 0; i < 16; i += 2) {
+            const float p0 = __int2float_rn((int)v[i]) * sw, p1 = __int2float_rn((int)v[i + 1]) * sw;
+            const float si = odd ? s[i + 1] : s[i];
+            own[i / 2] = (odd ? p1 : p0) * si;
+            recv[i / 2] = __shfl_xor_sync(0xffffffffu, odd ? p0 : p1, 1) * si;
+        }
+        uint16_t h[8];
+#pragma unroll
+        for (int i = 0; i < 8; ++i) h[i] = bf16_bits(w8_silu_mul(odd ? recv[i] : own[i], odd ? own[i] : recv[i]));
+#pragma unroll
+        for (int i = 0; i < 16; i += 2, out += 2 * pitch) st_if(valid && i + odd < ncol, out, h[i / 2]);
     }
 }
 
-template <int kOut>
-__device__ __forceinline__ void w8_store(const uint32_t (&v)[32], float sw, float bias, const float* sa, int ncol, bool valid, int odd,
-                                         char* out, size_t pitch) {
-    if (ncol == 32)
-        w8_store_chunk<kOut, true>(v, sw, bias, sa, ncol, valid, odd, out, pitch);
-    else
-        w8_store_chunk<kOut, false>(v, sw, bias, sa, ncol, valid, odd, out, pitch);
+// What a warp needs to write its part of a tile.
+struct W8Out {
+    float sw, bias;
+    const float* sa;  // lane l's scale of each of its chunks of 32 tokens (registers)
+    float* sa_w;      // 32 floats of shared memory of this warp (broadcast reads instead of a shuffle per token)
+    uint32_t acc;     // tensor-memory address of the accumulator, this warp's lanes
+    int c0;           // its first token; chunks of 32 are 64 apart
+    int row0, nrows, n, odd;
+};
+
+template <int CG, int kOut>
+__device__ __forceinline__ void w8_write_tile(const W8Args& a, const W8Out& o) {
+    constexpr bool kPair = kOut == kOutPairBf16 || kOut == kOutPairF16;
+    constexpr int kEl = kOut == kOutF32 || kOut == kOutI32 ? 4 : 2;
+    const int lane = threadIdx.x & 31;
+    const size_t pitch = (size_t)a.ldo * kEl;
+    char* out = static_cast<char*>(a.out) + (size_t)(o.row0 + o.c0 + (kPair || kOut == kOutSwiglu ? o.odd : 0)) * pitch +
+                (size_t)(o.n - (kPair ? o.odd : 0)) * kEl;
+    const bool valid = o.n < a.nvalid;
+    // 16 tokens at a time, the next 16 loading meanwhile
+    uint32_t v[16];
+    if (o.c0 < o.nrows) tmem_ld16(o.acc + (uint32_t)o.c0, v);
+#pragma unroll 1
+    for (int c = 0, c0 = o.c0; c0 < o.nrows; ++c, c0 += 64, out += 64 * pitch) {
+        float sa = o.sa[0];
+#pragma unroll
+        for (int i = 1; i < CG * 2; ++i) sa = c == i ? o.sa[i] : sa;
+        __syncwarp();
+        o.sa_w[lane] = sa;
+        __syncwarp();
+#pragma unroll
+        for (int h = 0; h < 2; ++h) {
+            const int ncol = o.nrows - c0 - 16 * h;
+            if (h == 1 && ncol <= 0) break;
+            uint32_t x[16];
+            tmem_ld_wait();
+#pragma unroll
+            for (int i = 0; i < 16; ++i) x[i] = v[i];
+            const int next = c0 + (h == 0 ? 16 : 64);
+            if (next < o.nrows) tmem_ld16(o.acc + (uint32_t)next, v);
+            w8_store<kOut>(x, o.sw, o.bias, o.sa_w + 16 * h, ncol, valid, o.odd, out + (size_t)(16 * h) * pitch, pitch);
+        }
+    }
 }
 
 // kSplit (CG = 1, dense): the CTAs of a cluster share one tile, each taking a part of its K
@@ -516,33 +566,16 @@ __global__ void __launch_bounds__(kW8Threads, 1)
                 }
                 break;
             }
-#pragma unroll
-            for (int c = 0; c < CG * 2; ++c) {
-                const int c0 = half * 32 + c * 64;
-                if (c0 >= t.nrows) break;
-                const int ncol = min(32, t.nrows - c0);  // tokens of this chunk
-                uint32_t v[32];
-                tmem_ld32(tmem + ((uint32_t)(q * 32) << 16) + b * kAccCols + (uint32_t)c0, v);
-                float* sa_w = sa_s + warp * 32;  // this warp's own 32 (eight broadcast reads for a shuffle per token)
-                __syncwarp();
-                sa_w[lane] = sa_r[c];
-                __syncwarp();
-                tmem_ld_wait();
-                const int el = a.out_kind == kOutF32 || a.out_kind == kOutI32 ? 4 : 2;
-                const bool pair = a.out_kind == kOutPairBf16 || a.out_kind == kOutPairF16;
-                const size_t pitch = (size_t)a.ldo * el;
-                const int row = t.row0 + c0 + (pair || a.out_kind == kOutSwiglu ? odd : 0);
-                char* out = static_cast<char*>(a.out) + (size_t)row * pitch + (size_t)(n - (pair ? odd : 0)) * el;
-                const bool valid = n < a.nvalid;
-                switch (a.out_kind) {
-                    case kOutF32: w8_store<kOutF32>(v, sw, bias, sa_w, ncol, valid, odd, out, pitch); break;
-                    case kOutI32: w8_store<kOutI32>(v, sw, bias, sa_w, ncol, valid, odd, out, pitch); break;
-                    case kOutBf16: w8_store<kOutBf16>(v, sw, bias, sa_w, ncol, valid, odd, out, pitch); break;
-                    case kOutF16: w8_store<kOutF16>(v, sw, bias, sa_w, ncol, valid, odd, out, pitch); break;
-                    case kOutPairBf16: w8_store<kOutPairBf16>(v, sw, bias, sa_w, ncol, valid, odd, out, pitch); break;
-                    case kOutPairF16: w8_store<kOutPairF16>(v, sw, bias, sa_w, ncol, valid, odd, out, pitch); break;
-                    default: w8_store<kOutSwiglu>(v, sw, bias, sa_w, ncol, valid, odd, out, pitch); break;
-                }
+            const W8Out o = {sw, bias, sa_r, sa_s + warp * 32, tmem + ((uint32_t)(q * 32) << 16) + b * kAccCols, half * 32,
+                             t.row0, t.nrows, n, odd};
+            switch (a.out_kind) {
+                case kOutF32: w8_write_tile<CG, kOutF32>(a, o); break;
+                case kOutI32: w8_write_tile<CG, kOutI32>(a, o); break;
+                case kOutBf16: w8_write_tile<CG, kOutBf16>(a, o); break;
+                case kOutF16: w8_write_tile<CG, kOutF16>(a, o); break;
+                case kOutPairBf16: w8_write_tile<CG, kOutPairBf16>(a, o); break;
+                case kOutPairF16: w8_write_tile<CG, kOutPairF16>(a, o); break;
+                default: w8_write_tile<CG, kOutSwiglu>(a, o); break;
             }
             tc_fence_before();
             __syncwarp();

@@ -533,8 +533,9 @@ struct Chunk16 {
     float v[16];
 };
 
-__device__ __forceinline__ void load_chunk(const uint16_t* row, int len, int k0, Chunk16& c) {
-    if ((len & 15) == 0 && k0 + 16 <= len) {
+// (aligned: the row starts on 16 bytes, whatever its length)
+__device__ __forceinline__ void load_chunk(const uint16_t* row, int len, int k0, Chunk16& c, bool aligned = false) {
+    if ((aligned || (len & 15) == 0) && k0 + 16 <= len) {
         const uint4 p0 = *reinterpret_cast<const uint4*>(row + k0);
         const uint4 p1 = *reinterpret_cast<const uint4*>(row + k0 + 8);
         const uint32_t pw[8] = {p0.x, p0.y, p0.z, p0.w, p1.x, p1.y, p1.z, p1.w};
@@ -582,14 +583,14 @@ __device__ __forceinline__ void quant_row_cta(const TIn* row, int len, int Kp, i
         for (int c = 0; c < kCache; ++c) {
             const int ci = t + c * 128;
             if (ci < nch) {
-                load_chunk(row, len, ci * 16, cache[c]);
+                load_chunk(row, len, ci * 16, cache[c], kW8);
 #pragma unroll
                 for (int i = 0; i < 16; ++i) amax = fmaxf(amax, fabsf(cache[c].v[i]));
             }
         }
         for (int ci = t + kCache * 128; ci < nch; ci += 128) {
             Chunk16 tmp;
-            load_chunk(row, len, ci * 16, tmp);
+            load_chunk(row, len, ci * 16, tmp, kW8);
 #pragma unroll
             for (int i = 0; i < 16; ++i) amax = fmaxf(amax, fabsf(tmp.v[i]));
         }
@@ -624,7 +625,7 @@ __device__ __forceinline__ void quant_row_cta(const TIn* row, int len, int Kp, i
     }
     for (int ci = t + kCache * 128; ci < nch; ci += 128) {
         Chunk16 tmp;
-        if (row != nullptr) load_chunk(row, len, ci * 16, tmp);
+        if (row != nullptr) load_chunk(row, len, ci * 16, tmp, kW8);
         else {
 #pragma unroll
             for (int i = 0; i < 16; ++i) tmp.v[i] = 0.f;
@@ -670,14 +671,14 @@ __global__ void __launch_bounds__(128) act_scatter_kernel(const uint16_t* __rest
     for (int c = 0; c < kRowCache; ++c) {
         const int ci = t + c * 128;
         if (ci < nch) {
-            load_chunk(row, H, ci * 16, cache[c]);
+            load_chunk(row, H, ci * 16, cache[c], kW8 && (H & 7) == 0);
 #pragma unroll
             for (int i = 0; i < 16; ++i) amax = fmaxf(amax, fabsf(cache[c].v[i]));
         }
     }
     for (int ci = t + kRowCache * 128; ci < nch; ci += 128) {
         Chunk16 tmp;
-        load_chunk(row, H, ci * 16, tmp);
+        load_chunk(row, H, ci * 16, tmp, kW8 && (H & 7) == 0);
 #pragma unroll
         for (int i = 0; i < 16; ++i) amax = fmaxf(amax, fabsf(tmp.v[i]));
     }
@@ -709,7 +710,7 @@ __global__ void __launch_bounds__(128) act_scatter_kernel(const uint16_t* __rest
     }
     for (int ci = t + kRowCache * 128; ci < nch; ci += 128) {
         Chunk16 tmp;
-        load_chunk(row, H, ci * 16, tmp);
+        load_chunk(row, H, ci * 16, tmp, kW8 && (H & 7) == 0);
         emit(ci, tmp);
     }
     if (t < k && dst[t] >= 0) s[dst[t]] = sc;
@@ -725,7 +726,47 @@ __global__ void __launch_bounds__(128) requant_kernel(const uint16_t* __restrict
     grid_dep_wait();  // the previous kernel of the forward has completed
     const int r = blockIdx.x;
     if (r >= __ldg(poffs + E)) return;
+    if (kW8 && row_src[r] < 0) return;  // (a pad row's codes and scale reach no output that is stored)
     quant_row_cta<kCache, kW8, uint16_t>(row_src[r] < 0 ? nullptr : h + (size_t)r * ldh, F, Kp, r, RB, act, s);
+}
+
+// The W8A8 layer's requantisation of short rows (F <= 512 * kChunks): a warp per row, which
+// stays in registers.  With F = 256 a CTA per row spends its time on being launched: 12000
+// rows 20 us, a warp each 8 us.
+template <int kChunks>
+__global__ void __launch_bounds__(256) requant_short_kernel(const uint16_t* __restrict__ h, int ldh, int F, int Kp,
+                                                            const int* __restrict__ row_src, const int* __restrict__ poffs,
+                                                            int E, int RB, int8_t* __restrict__ act, float* __restrict__ s) {
+    grid_dep_launch();
+    grid_dep_wait();
+    const int r = blockIdx.x * 8 + (threadIdx.x >> 5), lane = threadIdx.x & 31;
+    if (r >= __ldg(poffs + E) || row_src[r] < 0) return;
+    const uint16_t* row = h + (size_t)r * ldh;
+    const int nch = Kp / 16;
+    Chunk16 c[kChunks];
+    float amax = 0.f;
+#pragma unroll
+    for (int q = 0; q < kChunks; ++q)
+        if (lane + 32 * q < nch) {
+            load_chunk(row, F, (lane + 32 * q) * 16, c[q], true);
+#pragma unroll
+            for (int i = 0; i < 16; ++i) amax = fmaxf(amax, fabsf(c[q].v[i]));
+        }
+    amax = warp_max(amax);
+    const float sc = row_scale<true>(amax);
+    const float rinv = __fdiv_rn(1.0f, sc);
+#pragma unroll
+    for (int q = 0; q < kChunks; ++q) {
+        const int ci = lane + 32 * q;
+        if (ci >= nch) continue;
+        uint32_t out[4] = {0u, 0u, 0u, 0u};
+        if (amax > 0.f) {
+#pragma unroll
+            for (int i = 0; i < 16; ++i) out[i >> 2] |= (uint32_t)(quant_i8_fast(c[q].v[i], sc, rinv) & 0xFF) << (8 * (i & 3));
+        }
+        *reinterpret_cast<uint4*>(act + act_offset(r, ci * 16, Kp / kGroup, RB)) = make_uint4(out[0], out[1], out[2], out[3]);
+    }
+    if (lane == 0) s[r] = sc;
 }
 
 // ---------------------------------------------------------------------------
@@ -780,7 +821,7 @@ __global__ void __launch_bounds__(256) w8_prepare_kernel(const int32_t* __restri
     Chunk16 cache[2];
 #pragma unroll
     for (int c = 0; c < 2; ++c)
-        if (tid + c * 256 < nch) load_chunk(row, H, (tid + c * 256) * 16, cache[c]);
+        if (tid + c * 256 < nch) load_chunk(row, H, (tid + c * 256) * 16, cache[c], (H & 7) == 0);
     if (tid == 0) s_bad = 0;
     for (int e = tid; e < E; e += 256) s_off[e] = 0;
     __syncthreads();
@@ -859,7 +900,7 @@ __global__ void __launch_bounds__(256) w8_prepare_kernel(const int32_t* __restri
         }
     for (int ci = tid + 512; ci < nch; ci += 256) {
         Chunk16 tmp;
-        load_chunk(row, H, ci * 16, tmp);
+        load_chunk(row, H, ci * 16, tmp, (H & 7) == 0);
 #pragma unroll
         for (int i = 0; i < 16; ++i) amax = fmaxf(amax, fabsf(tmp.v[i]));
     }
@@ -885,7 +926,7 @@ __global__ void __launch_bounds__(256) w8_prepare_kernel(const int32_t* __restri
         if (tid + c * 256 < nch) emit(tid + c * 256, cache[c]);
     for (int ci = tid + 512; ci < nch; ci += 256) {
         Chunk16 tmp;
-        load_chunk(row, H, ci * 16, tmp);
+        load_chunk(row, H, ci * 16, tmp, (H & 7) == 0);
         emit(ci, tmp);
     }
     if (tid < k && dst[tid] >= 0) s[dst[tid]] = sc;
@@ -909,7 +950,7 @@ __global__ void __launch_bounds__(256) combine_kernel(const float* __restrict__ 
     }
     __syncthreads();
     const bool vec = (H & 7) == 0;
-    for (int c0 = threadIdx.x * 8; c0 < H; c0 += blockDim.x * 8) {
+    for (int c0 = (blockIdx.y * blockDim.x + threadIdx.x) * 8; c0 < H; c0 += gridDim.y * blockDim.x * 8) {
         float acc[8];
 #pragma unroll
         for (int i = 0; i < 8; ++i) acc[i] = 0.f;
@@ -1060,12 +1101,12 @@ cudaError_t launch_route_topk(const uint16_t* logits, int T, int E, int k, int32
     return launch_pdl(route_topk_kernel, ceil_div(T, 8), 256, 0, stream, logits, T, E, k, ids, w);
 }
 
-int perm_launch_count(int nslots) { return nslots <= kPermSmallSlots ? 1 : 3; }
+int perm_launch_count(int nslots, int small_slots) { return nslots <= small_slots ? 1 : 3; }
 
 cudaError_t launch_perm(const int32_t* ids, int nslots, int E, int tile_tokens, int* chist, int nchunk, int* counts,
                         int* offs, int* poffs, int* mtstart, int4* mt_tab, int* perm, int* inv, int* row_src,
-                        uint32_t* err, cudaStream_t stream) {
-    if (nslots <= kPermSmallSlots) {
+                        uint32_t* err, cudaStream_t stream, int small_slots) {
+    if (nslots <= small_slots) {
         const size_t smem = (size_t)35 * E * sizeof(int);
         static int attr_done[64] = {0};
         int dev = 0;
@@ -1105,6 +1146,9 @@ cudaError_t launch_w8_prepare(const int32_t* ids, const uint16_t* x, int T, int 
 cudaError_t launch_requant(const uint16_t* h, int ldh, int F, int Kp, const int* row_src, const int* poffs, int E,
                            int rows_cap, int rb, int8_t* act, float* s, cudaStream_t stream, bool w8) {
     if (rows_cap == 0) return cudaSuccess;
+    if (w8 && F <= 1024)
+        return launch_pdl(F <= 512 ? requant_short_kernel<1> : requant_short_kernel<2>, ceil_div(rows_cap, 8), 256, 0, stream, h,
+                          ldh, F, Kp, row_src, poffs, E, rb, act, s);
     const auto kernel = F <= 128 * 16 ? (w8 ? requant_kernel<1, true> : requant_kernel<1, false>)
                                       : (w8 ? requant_kernel<kRowCache, true> : requant_kernel<kRowCache, false>);
     return launch_pdl(kernel, rows_cap, 128, 0, stream, h, ldh, F, Kp, row_src, poffs, E, rb, act, s);
@@ -1113,7 +1157,9 @@ cudaError_t launch_requant(const uint16_t* h, int ldh, int F, int Kp, const int*
 cudaError_t launch_combine(const float* y2, int H, const int* inv, const float* w, int T, int k, uint16_t* out,
                            cudaStream_t stream, bool w8) {
     if (T == 0) return cudaSuccess;
-    return launch_pdl(w8 ? combine_kernel<true> : combine_kernel<false>, T, 256, 0, stream, y2, H, inv, w, T, k, out);
+    // W8A8: few tokens are spread over several CTAs each
+    const dim3 grid(T, w8 && T < 2 * sm_count() ? ceil_div(H, 256 * 8) : 1);
+    return launch_pdl(w8 ? combine_kernel<true> : combine_kernel<false>, grid, 256, 0, stream, y2, H, inv, w, T, k, out);
 }
 
 cudaError_t launch_dense_prep(const int8_t* qa, int M, int Kq, int Kp, int tile_tokens, int rb, int8_t* act, int4* mt_tab,

@@ -100,9 +100,12 @@ cudaError_t launch_route_experts(const void* logits, int type, int T, int E, int
                                  int topk_group, float scale, int32_t* ids, float* w, cudaStream_t stream);
 
 // MoE pipeline pieces
+constexpr int kPermChunk = 256;       // slots per permutation chunk (multi-CTA path)
+constexpr int kPermSmallSlots = 16384;  // up to this many slots the permutation runs in one CTA
+int perm_launch_count(int nslots, int small_slots = kPermSmallSlots);
 cudaError_t launch_perm(const int32_t* ids, int nslots, int E, int tile_tokens, int* chist, int nchunk, int* counts,
                         int* offs, int* poffs, int* mtstart, int4* mt_tab, int* perm, int* inv, int* row_src,
-                        uint32_t* err, cudaStream_t stream);
+                        uint32_t* err, cudaStream_t stream, int small_slots = kPermSmallSlots);
 // capacity of the row-tile table for a layer: sum over experts of ceil(count / tile)
 // <= nslots / tile + E, with tiles of at least 16 rows
 inline int mt_tab_capacity(int nslots, int E) { return nslots / 16 + E + 1; }
@@ -136,9 +139,6 @@ cudaError_t launch_dense_prep_bf16(const uint16_t* x, int M, int K, uint8_t* act
 cudaError_t launch_act_gather_bf16(const uint16_t* x, int T, int H, int k, const int* inv, uint8_t* x16, uint8_t* h16,
                                    int F, cudaStream_t stream);
 
-constexpr int kPermChunk = 256;       // slots per permutation chunk (multi-CTA path)
-constexpr int kPermSmallSlots = 16384;  // up to this many slots the permutation runs in one CTA
-int perm_launch_count(int nslots);
 
 // INT8 KV cache (kv_int8.cu)
 int kv_max_heads();

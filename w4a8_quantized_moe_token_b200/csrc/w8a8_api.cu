@@ -174,9 +174,9 @@ W4A8_EXPORT int w8a8_moe_forward(const void* packed_up, const void* packed_down,
                                  at<int4>(ws, L, R_MTTAB), at<int>(ws, L, R_PERM), inv, row_src, L.R, act1, s1, err, st));
     } else {
         {
-            ProfScope p(W4A8_KERNEL_PERM, perm_launch_count(L.nslots), st);
+            ProfScope p(W4A8_KERNEL_PERM, perm_launch_count(L.nslots, kPrepareSlots), st);
             W8_TRY(launch_perm(ids, L.nslots, E, plan.bn, at<int>(ws, L, R_CHIST), L.nchunk, at<int>(ws, L, R_COUNTS), offs,
-                               poffs, mtstart, at<int4>(ws, L, R_MTTAB), at<int>(ws, L, R_PERM), inv, row_src, err, st));
+                               poffs, mtstart, at<int4>(ws, L, R_MTTAB), at<int>(ws, L, R_PERM), inv, row_src, err, st, kPrepareSlots));
         }
         ProfScope p(W4A8_KERNEL_ACT_QUANT, 1, st);
         W8_TRY(launch_act_scatter(x, T, H, L.Hp, k, inv, offs, poffs, E, L.R, act1, s1, st, true));
