@@ -47,6 +47,7 @@ constexpr int kW8MaxStages = 12;
 // token scales
 constexpr int kW8BarBytes = (2 * kW8MaxStages + 5) * 8 + 16 + kW8EpiWarps * 32 * 4;  // + token scales
 constexpr int kW8SmemMax = 227 * 1024 - 1024;  // without the alignment slack
+constexpr int kW8SplitSmem = 48 * 1024;        // five do not fit into an SM's 228 KB
 inline int w8_smem(int ns, int b_stage, int recv) { return ns * (kW8BlockBytes + b_stage) + recv + kW8BarBytes + 1024; }
 
 // ---- PTX ----
@@ -358,13 +359,16 @@ __device__ __forceinline__ void w8_write_tile(const W8Args& a, const W8Out& o) {
 // kSplit (CG = 1, dense): the CTAs of a cluster share one tile, each taking a part of its K
 // planes.  Every CTA sends the INT32 partials of its peers' tokens into their shared memory
 // (st.async, counted by the receiver's barrier) and finishes its own share of the tokens:
-// exact sums, so the result does not depend on the
-// split, no workspace and no second launch.
+// exact sums, so the result does not depend on the split, no workspace and no second launch.
+// Several such CTAs may share an SM, and each waits for its peers while it holds its 128
+// columns of tensor memory; a peer that had to wait for columns could close a circle.  So the
+// launcher asks for enough shared memory that no more than four fit on an SM (512 columns).
 template <int CG, bool kSplit>
 __global__ void __launch_bounds__(kW8Threads, 1)
     gemm_w8a8_kernel(const __grid_constant__ CUtensorMap map_w, const __grid_constant__ CUtensorMap map_x,
                      const __grid_constant__ CUtensorMap map_small, const W8Args a) {
-    constexpr uint32_t kAccCols = 128 * CG;  // columns of one of the two accumulators
+    constexpr uint32_t kAccCols = 128 * CG;  // columns of an accumulator
+    constexpr uint32_t kTmemCols = kSplit ? kAccCols : 2 * kAccCols;
     extern __shared__ uint8_t smem_raw[];
     const uint32_t raw_addr = smem_u32(smem_raw);
     const uint32_t base = (raw_addr + 1023u) & ~1023u;
@@ -397,7 +401,7 @@ __global__ void __launch_bounds__(kW8Threads, 1)
         if (lane == 0) asm volatile("prefetch.tensormap [%0];" ::"l"(&map_w) : "memory");
         if (lane == 1) asm volatile("prefetch.tensormap [%0];" ::"l"(&map_x) : "memory");
     }
-    if (warp == kW8MmaWarp) w8_tmem_alloc<CG>(smem_u32(tmem_slot), 2 * kAccCols);
+    if (warp == kW8MmaWarp) w8_tmem_alloc<CG>(smem_u32(tmem_slot), kTmemCols);
     tc_fence_before();
     __syncthreads();
     if (CG == 2) cluster_sync();
@@ -610,7 +614,7 @@ __global__ void __launch_bounds__(kW8Threads, 1)
     }
     if (warp == kW8MmaWarp) {
         tc_fence_after();
-        w8_tmem_dealloc<CG>(tmem, 2 * kAccCols);
+        w8_tmem_dealloc<CG>(tmem, kTmemCols);
     }
 }
 
@@ -935,7 +939,8 @@ cudaError_t launch_gemm_w8a8(W8Args a, const W8Operands& op, const W8Plan* group
     if (a.ns > kW8MaxStages) a.ns = kW8MaxStages;
     const int steps = ceil_div(a.G, plan.split);  // a short K needs no more stages
     if (plan.split > 1 && a.ns > steps) a.ns = steps;
-    const int smem = w8_smem(a.ns, (int)a.b_stage, (int)a.recv);
+    int smem = w8_smem(a.ns, (int)a.b_stage, (int)a.recv);
+    if (plan.split > 1 && smem < kW8SplitSmem) smem = kW8SplitSmem;
     if (num_ctas > kW8StatusWords) num_ctas = kW8StatusWords;
     if (plan.split > 1) {
         const int grid = ceil_div(a.M, plan.bn) * a.NT * plan.split;
