@@ -638,13 +638,11 @@ __device__ __forceinline__ void quant_row_cta(const TIn* row, int len, int Kp, i
 // x rows (bf16) -> INT8 rows in expert-grouped order.  CTA t < T quantises token t
 // once (one read of x) and writes the codes to each of its k grouped rows; CTA T + e
 // writes zero codes and scale 0 into the pad rows of expert e.
-template <bool kW8>
 __global__ void __launch_bounds__(128) act_scatter_kernel(const uint16_t* __restrict__ x, int T, int H, int Kp, int k,
                                                           const int* __restrict__ inv,
                                                           const int* __restrict__ offs,
                                                           const int* __restrict__ poffs, int RB,
                                                           int8_t* __restrict__ act, float* __restrict__ s) {
-    if (kW8) grid_dep_launch();
     grid_dep_wait();  // the previous kernel of the forward has completed
     const int nch = Kp / 16;
     const int G = Kp / kGroup;
@@ -671,14 +669,14 @@ __global__ void __launch_bounds__(128) act_scatter_kernel(const uint16_t* __rest
     for (int c = 0; c < kRowCache; ++c) {
         const int ci = t + c * 128;
         if (ci < nch) {
-            load_chunk(row, H, ci * 16, cache[c], kW8 && (H & 7) == 0);
+            load_chunk(row, H, ci * 16, cache[c]);
 #pragma unroll
             for (int i = 0; i < 16; ++i) amax = fmaxf(amax, fabsf(cache[c].v[i]));
         }
     }
     for (int ci = t + kRowCache * 128; ci < nch; ci += 128) {
         Chunk16 tmp;
-        load_chunk(row, H, ci * 16, tmp, kW8 && (H & 7) == 0);
+        load_chunk(row, H, ci * 16, tmp);
 #pragma unroll
         for (int i = 0; i < 16; ++i) amax = fmaxf(amax, fabsf(tmp.v[i]));
     }
@@ -686,7 +684,7 @@ __global__ void __launch_bounds__(128) act_scatter_kernel(const uint16_t* __rest
     if ((t & 31) == 0) red[t >> 5] = amax;
     __syncthreads();
     amax = fmaxf(fmaxf(red[0], red[1]), fmaxf(red[2], red[3]));
-    const float sc = row_scale<kW8>(amax);
+    const float sc = __fdiv_rn(amax, 127.0f);
     const float rinv = __fdiv_rn(1.0f, sc);
     auto emit = [&](int ci, const Chunk16& c) {
         uint32_t out[4] = {0u, 0u, 0u, 0u};
@@ -710,7 +708,7 @@ __global__ void __launch_bounds__(128) act_scatter_kernel(const uint16_t* __rest
     }
     for (int ci = t + kRowCache * 128; ci < nch; ci += 128) {
         Chunk16 tmp;
-        load_chunk(row, H, ci * 16, tmp, kW8 && (H & 7) == 0);
+        load_chunk(row, H, ci * 16, tmp);
         emit(ci, tmp);
     }
     if (t < k && dst[t] >= 0) s[dst[t]] = sc;
@@ -730,9 +728,76 @@ __global__ void __launch_bounds__(128) requant_kernel(const uint16_t* __restrict
     quant_row_cta<kCache, kW8, uint16_t>(row_src[r] < 0 ? nullptr : h + (size_t)r * ldh, F, Kp, r, RB, act, s);
 }
 
-// The W8A8 layer's requantisation of short rows (F <= 512 * kChunks): a warp per row, which
-// stays in registers.  With F = 256 a CTA per row spends its time on being launched: 12000
-// rows 20 us, a warp each 8 us.
+// ---------------------------------------------------------------------------
+// W8A8 layer: rows kept as the bf16 pairs that were loaded, 16 values (two 16-byte words) at a
+// time, and quantised with a rounding constant.
+// ---------------------------------------------------------------------------
+struct Raw16 {
+    uint32_t w[8];
+};
+
+// 16 values of a row from k0 on, zero past len (aligned: the row starts on 16 bytes)
+__device__ __forceinline__ void load_raw(const uint16_t* row, int len, int k0, bool aligned, Raw16& c) {
+    if (aligned && k0 + 16 <= len) {
+        const uint4 p0 = *reinterpret_cast<const uint4*>(row + k0);
+        const uint4 p1 = *reinterpret_cast<const uint4*>(row + k0 + 8);
+        c.w[0] = p0.x; c.w[1] = p0.y; c.w[2] = p0.z; c.w[3] = p0.w;
+        c.w[4] = p1.x; c.w[5] = p1.y; c.w[6] = p1.z; c.w[7] = p1.w;
+    } else {
+#pragma unroll
+        for (int i = 0; i < 8; ++i) {
+            const uint32_t lo = k0 + 2 * i < len ? row[k0 + 2 * i] : 0u, hi = k0 + 2 * i + 1 < len ? row[k0 + 2 * i + 1] : 0u;
+            c.w[i] = lo | (hi << 16);
+        }
+    }
+}
+
+// the larger of amax and the chunk's magnitudes (NaN are passed over)
+__device__ __forceinline__ float raw_amax(const Raw16& c, float amax) {
+#pragma unroll
+    for (int i = 0; i < 8; ++i)
+        amax = fmaxf(amax, fmaxf(fabsf(__uint_as_float(c.w[i] << 16)), fabsf(__uint_as_float(c.w[i] & 0xFFFF0000u))));
+    return amax;
+}
+
+// INT8 codes of 16 values, the codes of quant_i8 bit for bit, where no |value| exceeds the
+// amax behind sc (so that nothing saturates).  t = x * inv + 1.5 * 2^23 holds rint(x * inv) in
+// its low bits; a value within 6.1e-5 of a rounding boundary (see quant_i8_fast), or not
+// finite, sends the chunk to the exact divisions: five instructions per value instead of
+// twelve.
+__device__ __forceinline__ uint4 quant16(const Raw16& c, float sc, float inv) {
+    constexpr float kMagic = 12582912.0f;
+    uint32_t out[4];
+    bool exact = false;
+#pragma unroll
+    for (int g = 0; g < 4; ++g) {
+        uint32_t b[4];
+#pragma unroll
+        for (int i = 0; i < 4; ++i) {
+            const uint32_t w = c.w[2 * g + i / 2];
+            const float y = __fmul_rn(__uint_as_float((i & 1) ? (w & 0xFFFF0000u) : (w << 16)), inv);
+            const float t = __fadd_rn(y, kMagic);
+            exact = exact || !(fabsf(__fsub_rn(y, __fsub_rn(t, kMagic))) < 0.5f - 6.103515625e-05f);
+            b[i] = __float_as_uint(t);
+        }
+        out[g] = __byte_perm(__byte_perm(b[0], b[1], 0x0040), __byte_perm(b[2], b[3], 0x0040), 0x5410);
+    }
+    if (exact) {
+#pragma unroll
+        for (int g = 0; g < 4; ++g) {
+            out[g] = 0u;
+#pragma unroll
+            for (int i = 0; i < 4; ++i) {
+                const uint32_t w = c.w[2 * g + i / 2];
+                out[g] |= (uint32_t)(quant_i8(__uint_as_float((i & 1) ? (w & 0xFFFF0000u) : (w << 16)), sc) & 0xFF) << (8 * i);
+            }
+        }
+    }
+    return make_uint4(out[0], out[1], out[2], out[3]);
+}
+
+// Requantisation of short rows (F <= 512 * kChunks): a warp per row, which stays in registers.
+// (With F = 256 a CTA per row spends its time on being launched: 12000 rows 20 us, so 12 us.)
 template <int kChunks>
 __global__ void __launch_bounds__(256) requant_short_kernel(const uint16_t* __restrict__ h, int ldh, int F, int Kp,
                                                             const int* __restrict__ row_src, const int* __restrict__ poffs,
@@ -740,37 +805,35 @@ __global__ void __launch_bounds__(256) requant_short_kernel(const uint16_t* __re
     grid_dep_launch();
     grid_dep_wait();
     const int r = blockIdx.x * 8 + (threadIdx.x >> 5), lane = threadIdx.x & 31;
-    if (r >= __ldg(poffs + E) || row_src[r] < 0) return;
     const uint16_t* row = h + (size_t)r * ldh;
     const int nch = Kp / 16;
-    Chunk16 c[kChunks];
+    const bool exists = r < __ldg(poffs + E);  // (false: inside the workspace all the same, or past it)
+    if (!exists) return;
+    const int src = row_src[r];  // (a pad row is read, not written)
+    Raw16 c[kChunks];
     float amax = 0.f;
 #pragma unroll
     for (int q = 0; q < kChunks; ++q)
-        if (lane + 32 * q < nch) {
-            load_chunk(row, F, (lane + 32 * q) * 16, c[q], true);
+        if (lane + 32 * q < nch) load_raw(row, F, (lane + 32 * q) * 16, true, c[q]);
+    if (src < 0) return;
 #pragma unroll
-            for (int i = 0; i < 16; ++i) amax = fmaxf(amax, fabsf(c[q].v[i]));
-        }
+    for (int q = 0; q < kChunks; ++q)
+        if (lane + 32 * q < nch) amax = raw_amax(c[q], amax);
     amax = warp_max(amax);
     const float sc = row_scale<true>(amax);
     const float rinv = __fdiv_rn(1.0f, sc);
 #pragma unroll
     for (int q = 0; q < kChunks; ++q) {
         const int ci = lane + 32 * q;
-        if (ci >= nch) continue;
-        uint32_t out[4] = {0u, 0u, 0u, 0u};
-        if (amax > 0.f) {
-#pragma unroll
-            for (int i = 0; i < 16; ++i) out[i >> 2] |= (uint32_t)(quant_i8_fast(c[q].v[i], sc, rinv) & 0xFF) << (8 * (i & 3));
-        }
-        *reinterpret_cast<uint4*>(act + act_offset(r, ci * 16, Kp / kGroup, RB)) = make_uint4(out[0], out[1], out[2], out[3]);
+        if (ci < nch)
+            *reinterpret_cast<uint4*>(act + act_offset(r, ci * 16, Kp / kGroup, RB)) =
+                amax > 0.f ? quant16(c[q], sc, rinv) : make_uint4(0u, 0u, 0u, 0u);
     }
     if (lane == 0) s[r] = sc;
 }
 
-// The W8A8 layer's activation quantisation of short rows (H <= 512 * kChunks): a warp per token,
-// its row in registers, written to the token's k places.
+// Activation quantisation of short rows (H <= 512 * kChunks): a warp per token, its row in
+// registers, written to the token's k places.
 template <int kChunks>
 __global__ void __launch_bounds__(256) act_scatter_short_kernel(const uint16_t* __restrict__ x, int T, int H, int Kp, int k,
                                                                 const int* __restrict__ inv, int RB, int8_t* __restrict__ act,
@@ -782,33 +845,85 @@ __global__ void __launch_bounds__(256) act_scatter_short_kernel(const uint16_t* 
     const uint16_t* row = x + (size_t)tok * H;
     const int nch = Kp / 16, G = Kp / kGroup;
     const int my_dst = lane < k ? __ldg(inv + (size_t)tok * k + lane) : -1;
-    Chunk16 c[kChunks];
+    Raw16 c[kChunks];
     float amax = 0.f;
 #pragma unroll
     for (int q = 0; q < kChunks; ++q)
-        if (lane + 32 * q < nch) {
-            load_chunk(row, H, (lane + 32 * q) * 16, c[q], (H & 7) == 0);
+        if (lane + 32 * q < nch) load_raw(row, H, (lane + 32 * q) * 16, (H & 7) == 0, c[q]);
 #pragma unroll
-            for (int i = 0; i < 16; ++i) amax = fmaxf(amax, fabsf(c[q].v[i]));
-        }
+    for (int q = 0; q < kChunks; ++q)
+        if (lane + 32 * q < nch) amax = raw_amax(c[q], amax);
     amax = warp_max(amax);
     const float sc = row_scale<true>(amax);
     const float rinv = __fdiv_rn(1.0f, sc);
 #pragma unroll
     for (int q = 0; q < kChunks; ++q) {
         const int ci = lane + 32 * q;
-        uint32_t out[4] = {0u, 0u, 0u, 0u};
-        if (ci < nch && amax > 0.f) {
-#pragma unroll
-            for (int i = 0; i < 16; ++i) out[i >> 2] |= (uint32_t)(quant_i8_fast(c[q].v[i], sc, rinv) & 0xFF) << (8 * (i & 3));
-        }
+        const uint4 o = ci < nch && amax > 0.f ? quant16(c[q], sc, rinv) : make_uint4(0u, 0u, 0u, 0u);
         for (int j = 0; j < k; ++j) {
             const int r = __shfl_sync(0xffffffffu, my_dst, j);
-            if (r >= 0 && ci < nch)
-                *reinterpret_cast<uint4*>(act + act_offset(r, ci * 16, G, RB)) = make_uint4(out[0], out[1], out[2], out[3]);
+            if (r >= 0 && ci < nch) *reinterpret_cast<uint4*>(act + act_offset(r, ci * 16, G, RB)) = o;
         }
     }
     if (my_dst >= 0) s[my_dst] = sc;
+}
+
+// The quantisation of one row by a CTA of 256 threads, written to the places dst[0 .. k): two
+// chunks per thread in registers (loaded by the caller), longer rows read again.
+__device__ __forceinline__ void quant_row_places(const uint16_t* row, int H, int Kp, int k, const Raw16 (&cache)[2],
+                                                 const int* dst, float* red, int RB, int8_t* __restrict__ act,
+                                                 float* __restrict__ s) {
+    const int tid = threadIdx.x, nch = Kp / 16, G = Kp / kGroup;
+    const bool aligned = (H & 7) == 0;
+    float amax = 0.f;
+#pragma unroll
+    for (int c = 0; c < 2; ++c)
+        if (tid + c * 256 < nch) amax = raw_amax(cache[c], amax);
+    for (int ci = tid + 512; ci < nch; ci += 256) {
+        Raw16 tmp;
+        load_raw(row, H, ci * 16, aligned, tmp);
+        amax = raw_amax(tmp, amax);
+    }
+    amax = warp_max(amax);
+    if ((tid & 31) == 0) red[tid >> 5] = amax;
+    __syncthreads();  // (dst, too, is complete)
+#pragma unroll
+    for (int w = 0; w < 8; ++w) amax = fmaxf(amax, red[w]);
+    const float sc = row_scale<true>(amax);
+    const float rinv = __fdiv_rn(1.0f, sc);
+    auto emit = [&](int ci, const Raw16& c) {
+        const uint4 q = amax > 0.f ? quant16(c, sc, rinv) : make_uint4(0u, 0u, 0u, 0u);
+        for (int j = 0; j < k; ++j)
+            if (dst[j] >= 0) *reinterpret_cast<uint4*>(act + act_offset(dst[j], ci * 16, G, RB)) = q;
+    };
+#pragma unroll
+    for (int c = 0; c < 2; ++c)
+        if (tid + c * 256 < nch) emit(tid + c * 256, cache[c]);
+    for (int ci = tid + 512; ci < nch; ci += 256) {
+        Raw16 tmp;
+        load_raw(row, H, ci * 16, aligned, tmp);
+        emit(ci, tmp);
+    }
+    if (tid < k && dst[tid] >= 0) s[dst[tid]] = sc;
+}
+
+// Activation quantisation, a CTA per token.  Pad rows are left alone: they reach no output
+// that is stored.
+__global__ void __launch_bounds__(256) act_scatter_w8_kernel(const uint16_t* __restrict__ x, int H, int Kp, int k,
+                                                             const int* __restrict__ inv, int RB, int8_t* __restrict__ act,
+                                                             float* __restrict__ s) {
+    grid_dep_launch();
+    grid_dep_wait();
+    __shared__ int dst[32];
+    __shared__ float red[8];
+    const int tid = threadIdx.x, nch = Kp / 16;
+    const uint16_t* row = x + (size_t)blockIdx.x * H;
+    Raw16 cache[2];
+#pragma unroll
+    for (int c = 0; c < 2; ++c)
+        if (tid + c * 256 < nch) load_raw(row, H, (tid + c * 256) * 16, (H & 7) == 0, cache[c]);
+    if (tid < k) dst[tid] = __ldg(inv + (size_t)blockIdx.x * k + tid);
+    quant_row_places(row, H, Kp, k, cache, dst, red, RB, act, s);
 }
 
 // ---------------------------------------------------------------------------
@@ -857,13 +972,13 @@ __global__ void __launch_bounds__(256) w8_prepare_kernel(const int32_t* __restri
     __shared__ float red[8];
     const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
     const int tok = blockIdx.x, nslots = T * k;
-    const int nch = Kp / 16, G = Kp / kGroup;
+    const int nch = Kp / 16;
     const uint16_t* row = x + (size_t)tok * H;
-    // the token's row: up to two chunks per thread in registers, loading while the ids are counted
-    Chunk16 cache[2];
+    // the token's row, loading while the ids are counted
+    Raw16 cache[2];
 #pragma unroll
     for (int c = 0; c < 2; ++c)
-        if (tid + c * 256 < nch) load_chunk(row, H, (tid + c * 256) * 16, cache[c], (H & 7) == 0);
+        if (tid + c * 256 < nch) load_raw(row, H, (tid + c * 256) * 16, (H & 7) == 0, cache[c]);
     if (tid == 0) s_bad = 0;
     for (int e = tid; e < E; e += 256) s_off[e] = 0;
     __syncthreads();
@@ -932,46 +1047,7 @@ __global__ void __launch_bounds__(256) w8_prepare_kernel(const int32_t* __restri
             }
         }
     }
-    // quantise the row and write it to its k places
-    float amax = 0.f;
-#pragma unroll
-    for (int c = 0; c < 2; ++c)
-        if (tid + c * 256 < nch) {
-#pragma unroll
-            for (int i = 0; i < 16; ++i) amax = fmaxf(amax, fabsf(cache[c].v[i]));
-        }
-    for (int ci = tid + 512; ci < nch; ci += 256) {
-        Chunk16 tmp;
-        load_chunk(row, H, ci * 16, tmp, (H & 7) == 0);
-#pragma unroll
-        for (int i = 0; i < 16; ++i) amax = fmaxf(amax, fabsf(tmp.v[i]));
-    }
-    amax = warp_max(amax);
-    if (lane == 0) red[warp] = amax;
-    __syncthreads();
-#pragma unroll
-    for (int w = 0; w < 8; ++w) amax = fmaxf(amax, red[w]);
-    const float sc = row_scale<true>(amax);
-    const float rinv = __fdiv_rn(1.0f, sc);
-    auto emit = [&](int ci, const Chunk16& c) {
-        uint32_t out[4] = {0u, 0u, 0u, 0u};
-        if (amax > 0.f) {
-#pragma unroll
-            for (int i = 0; i < 16; ++i) out[i >> 2] |= (uint32_t)(quant_i8_fast(c.v[i], sc, rinv) & 0xFF) << (8 * (i & 3));
-        }
-        const uint4 q = make_uint4(out[0], out[1], out[2], out[3]);
-        for (int j = 0; j < k; ++j)
-            if (dst[j] >= 0) *reinterpret_cast<uint4*>(act + act_offset(dst[j], ci * 16, G, RB)) = q;
-    };
-#pragma unroll
-    for (int c = 0; c < 2; ++c)
-        if (tid + c * 256 < nch) emit(tid + c * 256, cache[c]);
-    for (int ci = tid + 512; ci < nch; ci += 256) {
-        Chunk16 tmp;
-        load_chunk(row, H, ci * 16, tmp, (H & 7) == 0);
-        emit(ci, tmp);
-    }
-    if (tid < k && dst[tid] >= 0) s[dst[tid]] = sc;
+    quant_row_places(row, H, Kp, k, cache, dst, red, RB, act, s);
 }
 
 // ---------------------------------------------------------------------------
@@ -1174,15 +1250,12 @@ cudaError_t launch_perm(const int32_t* ids, int nslots, int E, int tile_tokens, 
 cudaError_t launch_act_scatter(const uint16_t* x, int T, int H, int Kp, int k, const int* inv, const int* offs,
                                const int* poffs, int E, int rb, int8_t* act, float* s, cudaStream_t stream, bool w8) {
     if (T == 0) return cudaSuccess;
-    // 3000 tokens of 1024 values to 4 places each: 14 us with a warp per token, 20 us with a CTA;
-    // at 2048 values (four chunks per lane) 26 against 22 us
-    if (w8 && H <= 1024) {
-        const auto kernel = H <= 512 ? act_scatter_short_kernel<1> : act_scatter_short_kernel<2>;
-        return launch_pdl(kernel, ceil_div(T, 8), 256, 0, stream, x, T, H, Kp, k, inv, rb, act, s);
-    }
-    // (W8A8: pad rows reach no output that is stored, they are left alone)
-    return launch_pdl(w8 ? act_scatter_kernel<true> : act_scatter_kernel<false>, w8 ? T : T + E, 128, 0, stream, x, T, H, Kp, k,
-                      inv, offs, poffs, rb, act, s);
+    // 3000 tokens of 1024 values to 4 places each: 14 us with a warp per token, 20 us with a CTA
+    if (w8 && H <= 1024)
+        return launch_pdl(H <= 512 ? act_scatter_short_kernel<1> : act_scatter_short_kernel<2>, ceil_div(T, 8), 256, 0, stream, x,
+                          T, H, Kp, k, inv, rb, act, s);
+    if (w8) return launch_pdl(act_scatter_w8_kernel, T, 256, 0, stream, x, H, Kp, k, inv, rb, act, s);
+    return launch_pdl(act_scatter_kernel, T + E, 128, 0, stream, x, T, H, Kp, k, inv, offs, poffs, rb, act, s);
 }
 
 cudaError_t launch_w8_prepare(const int32_t* ids, const uint16_t* x, int T, int H, int Kp, int k, int E, int tile_tokens,
@@ -1195,9 +1268,11 @@ cudaError_t launch_w8_prepare(const int32_t* ids, const uint16_t* x, int T, int 
 cudaError_t launch_requant(const uint16_t* h, int ldh, int F, int Kp, const int* row_src, const int* poffs, int E,
                            int rows_cap, int rb, int8_t* act, float* s, cudaStream_t stream, bool w8) {
     if (rows_cap == 0) return cudaSuccess;
-    if (w8 && F <= 1024)
-        return launch_pdl(F <= 512 ? requant_short_kernel<1> : requant_short_kernel<2>, ceil_div(rows_cap, 8), 256, 0, stream, h,
-                          ldh, F, Kp, row_src, poffs, E, rb, act, s);
+    if (w8 && F <= 2048)
+        return launch_pdl(F <= 512    ? requant_short_kernel<1>
+                          : F <= 1024 ? requant_short_kernel<2>
+                                      : requant_short_kernel<4>,
+                          ceil_div(rows_cap, 8), 256, 0, stream, h, ldh, F, Kp, row_src, poffs, E, rb, act, s);
     const auto kernel = F <= 128 * 16 ? (w8 ? requant_kernel<1, true> : requant_kernel<1, false>)
                                       : (w8 ? requant_kernel<kRowCache, true> : requant_kernel<kRowCache, false>);
     return launch_pdl(kernel, rows_cap, 128, 0, stream, h, ldh, F, Kp, row_src, poffs, E, rb, act, s);
