@@ -797,7 +797,8 @@ __device__ __forceinline__ uint4 quant16(const Raw16& c, float sc, float inv) {
 }
 
 // Requantisation of short rows (F <= 512 * kChunks): a warp per row, which stays in registers.
-// (With F = 256 a CTA per row spends its time on being launched: 12000 rows 20 us, so 12 us.)
+// (With F = 256 a CTA per row spends its time on being launched: 12000 rows 20 us, so 12 us;
+// launch_requant() has the rule and both sides at longer rows.)
 template <int kChunks>
 __global__ void __launch_bounds__(256) requant_short_kernel(const uint16_t* __restrict__ h, int ldh, int F, int Kp,
                                                             const int* __restrict__ row_src, const int* __restrict__ poffs,
@@ -1268,7 +1269,12 @@ cudaError_t launch_w8_prepare(const int32_t* ids, const uint16_t* x, int T, int 
 cudaError_t launch_requant(const uint16_t* h, int ldh, int F, int Kp, const int* row_src, const int* poffs, int E,
                            int rows_cap, int rb, int8_t* act, float* s, cudaStream_t stream, bool w8) {
     if (rows_cap == 0) return cudaSuccess;
-    if (w8 && F <= 2048)
+    // A warp per row up to F = 2048, unless a CTA per row fits the GPU at once and a row keeps
+    // most of a CTA busy (F > 1024). CTA against warp at F = 1408: 384 rows 8.7 against 10.7 us,
+    // 1536 rows 10.7 both, 3840 rows 14.6 against 12.8, 49152 rows (F = 1536) 140 against 84; at
+    // F = 2048: 1920 rows 11.1 against 12.9, 3840 rows 14.8 against 14.7; at F = 1024, 160 rows
+    // of 512 experts 10.8 against 8.8.
+    if (w8 && F <= 2048 && (F <= 1024 || rows_cap > 16 * sm_count()))
         return launch_pdl(F <= 512    ? requant_short_kernel<1>
                           : F <= 1024 ? requant_short_kernel<2>
                                       : requant_short_kernel<4>,
