@@ -362,7 +362,9 @@ __device__ __forceinline__ void w8_write_tile(const W8Args& a, const W8Out& o) {
 // exact sums, so the result does not depend on the split, no workspace and no second launch.
 // Several such CTAs may share an SM, and each waits for its peers while it holds its 128
 // columns of tensor memory; a peer that had to wait for columns could close a circle.  So the
-// launcher asks for enough shared memory that no more than four fit on an SM (512 columns).
+// launcher asks for enough shared memory that no more than four fit on an SM (512 columns),
+// and should another program's kernel hold columns there, the wait for the peer's data runs
+// out and frees this CTA's.
 template <int CG, bool kSplit>
 __global__ void __launch_bounds__(kW8Threads, 1)
     gemm_w8a8_kernel(const __grid_constant__ CUtensorMap map_w, const __grid_constant__ CUtensorMap map_x,
@@ -401,11 +403,12 @@ __global__ void __launch_bounds__(kW8Threads, 1)
         if (lane == 0) asm volatile("prefetch.tensormap [%0];" ::"l"(&map_w) : "memory");
         if (lane == 1) asm volatile("prefetch.tensormap [%0];" ::"l"(&map_x) : "memory");
     }
+    // (before the allocation: a peer that has to wait for its columns holds up data, not barriers)
+    if (kSplit) cluster_arrive();  // the epilogue warps wait, before they reach for their peers
     if (warp == kW8MmaWarp) w8_tmem_alloc<CG>(smem_u32(tmem_slot), kTmemCols);
     tc_fence_before();
     __syncthreads();
     if (CG == 2) cluster_sync();
-    if (kSplit) cluster_arrive();  // the epilogue warps wait, before they reach for their peers
     tc_fence_after();
     const uint32_t tmem = *tmem_slot;
 
@@ -604,6 +607,12 @@ __global__ void __launch_bounds__(kW8Threads, 1)
             while (clock64() - t0 < 100000) {
             }
         }
+        // (a split CTA frees its columns first: a peer may be waiting for some)
+        if (kSplit && warp == kW8MmaWarp) {
+            tc_fence_after();
+            w8_tmem_dealloc<CG>(tmem, kTmemCols);
+        }
+        __syncwarp();
         cluster_sync();
     }
     if (a.status != nullptr) {
@@ -612,7 +621,7 @@ __global__ void __launch_bounds__(kW8Threads, 1)
         if (blockIdx.x == 0)
             for (int i = (int)gridDim.x + (int)threadIdx.x; i < kW8StatusWords; i += kW8Threads) a.status[i] = 0u;
     }
-    if (warp == kW8MmaWarp) {
+    if (warp == kW8MmaWarp && !(kSplit && *abort_flag)) {
         tc_fence_after();
         w8_tmem_dealloc<CG>(tmem, kTmemCols);
     }
