@@ -2,6 +2,10 @@
 INT32 sums exact, the dense outputs within the counted roundings, the MoE layer within the
 layer tolerance, and the operators together as a serving step uses them."""
 
+import os
+import subprocess
+import sys
+
 import numpy as np
 import pytest
 import torch
@@ -287,6 +291,55 @@ def test_moe_zero_rows_and_outliers():
     assert_close_overall(got, ref)
 
 
+# rows longer than a thread's or a warp's registers hold, and both sides of each choice of
+# quantisation kernel: H > 8192 and F > 2048; F in (1024, 2048] with few and with many rows;
+# more than 2048 slots with H on both sides of 512 and 1024; odd lengths of each
+LONG_ROWS = [
+    (3, 2, 2, 8200, 16, "uniform"), (2, 2, 1, 8193, 9, "uniform"), (1100, 2, 2, 8200, 8, "uniform"),
+    (5, 2, 2, 64, 2100, "uniform"), (3, 2, 1, 40, 2049, "uniform"), (20, 2, 2, 128, 1100, "uniform"),
+    (1500, 2, 2, 72, 1100, "uniform"), (1300, 2, 2, 72, 2041, "zipf"), (1100, 3, 2, 513, 40, "uniform"),
+    (1100, 3, 2, 1024, 24, "uniform"), (1100, 3, 2, 1031, 513, "uniform"), (700, 3, 3, 1040, 1025, "zipf"),
+]
+
+
+@pytest.mark.parametrize("T,E,k,H,F,routing", LONG_ROWS)
+def test_moe_long_rows(T, E, k, H, F, routing):
+    L = Layer(T, E, k, H, F, routing, seed=3 * T + H)
+    L.run()
+
+
+@pytest.mark.parametrize("T,H", [(24, 256), (24, 257), (1100, 256), (1100, 1100), (1100, 515)])
+def test_moe_codes_next_to_a_rounding_boundary(T, H):
+    """Token rows whose quotients lie on or next to n + 1/2, rows of subnormal and of the
+    largest values, and rows with one value only: codes and
+    scales equal the oracle's bit by bit."""
+    L = Layer(T, 3, 2, H, 32, "uniform", seed=H + T)
+    rng = np.random.default_rng(T + H)
+    step = 2.0 ** rng.integers(-100, 20, (T, 1))
+    x = (rng.integers(-64, 64, (T, H)) + 0.5) * step
+    x[:, 0] = 127.0 * step[:, 0]  # the scale is the step, within one rounding
+    x[0::7] *= 2.0 ** -40         # some further down, into the subnormals
+    x[1::7] = np.sign(x[1::7]) * rng.integers(1, 128, x[1::7].shape) * 2.0 ** -133
+    x[2::7, 1:] = 0.0
+    x[3::7] = x[3::7] * 2.0 ** 100 / step[3::7]
+    L.x = synth.bf16_round(x.astype(np.float32))
+    L.w = (L.w * 2.0 ** -20).astype(np.float32)
+    qx, sx = W.quantize(L.x)
+    out = torch.empty((T, H), dtype=torch.bfloat16, device="cuda")
+    B.w8a8_moe_forward(*L.packed, L.E, H, L.F, dev_bf16(L.x), torch.from_numpy(L.ids).cuda(), torch.from_numpy(L.w).cuda(),
+                       out, L.ws)
+    torch.cuda.synchronize()
+
+    def dump(what, dt):
+        return B.w4a8_debug_dump(L.ws, T, L.E, L.k, H, L.F, what).cpu().numpy().view(dt)
+
+    row = dump("inv", np.int32)
+    act = untile_act(dump("act1", np.int8), B.w4a8_moe_rows_capacity(T, L.E, L.k), O.padded_k(H))
+    slots = np.arange(T * L.k)
+    assert np.array_equal(dump("s1", np.float32)[row], sx[slots // L.k])
+    assert np.array_equal(act[row], qx[slots // L.k])
+
+
 @pytest.mark.parametrize("M,N,K", [(16, 256, 640), (300, 256, 640), (1, 512, 4096)])
 def test_gemm_wait_timeout_is_reported_and_recovers(M, N, K):
     qa, sa, w, qw, sw, _ = dense_case(M, N, K)
@@ -394,3 +447,57 @@ def test_two_streams_at_once():
             b.run()
     torch.cuda.synchronize()
     a.check(), b.check()
+
+
+FIRST_CALL = """
+import sys
+import torch
+from w4a8_quantized_moe_token_b200 import binding as B
+
+def buf(n):
+    return B.empty_aligned(n)
+
+torch.manual_seed(0)
+E, H, F, k, T = 8, 256, 128, 2, {T}
+def pack(E, N, K, layout):
+    p = buf(B.w8a8_packed_bytes(E, N, K, layout))
+    B.w8a8_pack_weights(torch.randn(E, N, K, device="cuda").bfloat16(), layout, p)
+    return p
+up, dn, wn = pack(E, 2 * F, H, 1), pack(E, H, F, 0), pack(1, 256, H, 0)
+x = torch.randn(T, H, device="cuda").bfloat16()
+logits = torch.randn(T, E, device="cuda")
+ids, w = torch.empty(T, k, dtype=torch.int32, device="cuda"), torch.empty(T, k, device="cuda")
+out, y = torch.zeros(T, H, dtype=torch.bfloat16, device="cuda"), torch.zeros(T, 256, device="cuda")
+qa, sa = torch.empty(T, H, dtype=torch.int8, device="cuda"), torch.empty(T, device="cuda")
+B.w4a8_quant_act(x, qa, sa)
+ws, wd = buf(B.w8a8_moe_workspace_bytes(T, E, k, H, F)), buf(B.w8a8_gemm_workspace_bytes(T, 256, H))
+def run():
+    B.w4a8_route_experts(logits, k, ids, w)
+    B.w8a8_moe_forward(up, dn, E, H, F, x, ids, w, out, ws)
+    B.w8a8_gemm(qa, sa, wn, 256, H, y, wd)
+torch.cuda.synchronize()
+graph = torch.cuda.CUDAGraph()
+with torch.cuda.graph(graph):
+    run()
+graph.replay()
+torch.cuda.synchronize()
+got = [t.clone() for t in (ids, w, out, y)]
+run()
+torch.cuda.synchronize()
+assert all(torch.equal(a, b) for a, b in zip(got, (ids, w, out, y))) and out.abs().sum() > 0 and y.abs().sum() > 0
+"""
+
+
+@pytest.mark.parametrize("T", [1, 1100])
+def test_first_call_of_a_process_inside_a_capture(T):
+    root = os.path.dirname(os.path.dirname(os.path.abspath(__file__)))
+    r = subprocess.run([sys.executable, "-c", FIRST_CALL.replace("{T}", str(T))], cwd=root, capture_output=True, text=True,
+                       timeout=300)
+    assert r.returncode == 0, r.stderr[-2000:]
+
+
+def test_last_error_refuses_other_buffers():
+    with pytest.raises(B.W4A8Error):
+        B.w8a8_gemm_last_error(B.empty_aligned(2048))
+    with pytest.raises(B.W4A8Error):
+        B.w8a8_gemm_last_error(torch.zeros(4096, dtype=torch.uint8))

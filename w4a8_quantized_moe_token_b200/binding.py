@@ -551,6 +551,8 @@ def w8a8_gemm(qa, sa, packed, N, K, y, ws, bias=None):
 
 def w8a8_gemm_last_error(ws) -> int:
     """Device error word of the last w8a8_gemm call on this workspace (synchronises the stream)."""
+    _dev(ws, torch.uint8, "ws")
+    _need(ws.numel() >= w8a8_gemm_workspace_bytes(0, 1, 1), "ws is not a workspace of w8a8_gemm")
     r = lib().w8a8_gemm_last_error(_ptr(ws), _stream())
     if r < 0:
         _check(r, "w8a8_gemm_last_error")
