@@ -8,6 +8,7 @@
 #include <vector>
 
 #include "../../include/w4a8.h"
+#include "layer_internal.h"
 #include "w4a8_common.cuh"
 #include "w4a8_internal.h"
 

@@ -29,6 +29,7 @@
 #include <mutex>
 
 #include "../../include/w8a8.h"
+#include "layer_internal.h"
 #include "w4a8_common.cuh"
 #include "w8a8_internal.h"
 

@@ -11,6 +11,7 @@
 // division, so codes agree bit for bit with any other IEEE implementation.
 #include <climits>
 
+#include "layer_internal.h"
 #include "w4a8_common.cuh"
 #include "w4a8_internal.h"
 
@@ -798,7 +799,7 @@ __device__ __forceinline__ uint4 quant16(const Raw16& c, float sc, float inv) {
 
 // Requantisation of short rows (F <= 512 * kChunks): a warp per row, which stays in registers.
 // (With F = 256 a CTA per row spends its time on being launched: 12000 rows 20 us, so 12 us;
-// launch_requant() has the rule and both sides at longer rows.)
+// launch_w8_requant() has the rule and both sides at longer rows.)
 template <int kChunks>
 __global__ void __launch_bounds__(256) requant_short_kernel(const uint16_t* __restrict__ h, int ldh, int F, int Kp,
                                                             const int* __restrict__ row_src, const int* __restrict__ poffs,
@@ -1221,6 +1222,7 @@ cudaError_t launch_route_topk(const uint16_t* logits, int T, int E, int k, int32
 }
 
 int perm_launch_count(int nslots, int small_slots) { return nslots <= small_slots ? 1 : 3; }
+int perm_launch_count(int nslots) { return perm_launch_count(nslots, kPermSmallSlots); }
 
 cudaError_t launch_perm(const int32_t* ids, int nslots, int E, int tile_tokens, int* chist, int nchunk, int* counts,
                         int* offs, int* poffs, int* mtstart, int4* mt_tab, int* perm, int* inv, int* row_src,
@@ -1248,15 +1250,27 @@ cudaError_t launch_perm(const int32_t* ids, int nslots, int E, int tile_tokens, 
                       row_src);
 }
 
+cudaError_t launch_perm(const int32_t* ids, int nslots, int E, int tile_tokens, int* chist, int nchunk, int* counts,
+                        int* offs, int* poffs, int* mtstart, int4* mt_tab, int* perm, int* inv, int* row_src,
+                        uint32_t* err, cudaStream_t stream) {
+    return launch_perm(ids, nslots, E, tile_tokens, chist, nchunk, counts, offs, poffs, mtstart, mt_tab, perm, inv, row_src,
+                       err, stream, kPermSmallSlots);
+}
+
 cudaError_t launch_act_scatter(const uint16_t* x, int T, int H, int Kp, int k, const int* inv, const int* offs,
-                               const int* poffs, int E, int rb, int8_t* act, float* s, cudaStream_t stream, bool w8) {
+                               const int* poffs, int E, int rb, int8_t* act, float* s, cudaStream_t stream) {
+    if (T == 0) return cudaSuccess;
+    return launch_pdl(act_scatter_kernel, T + E, 128, 0, stream, x, T, H, Kp, k, inv, offs, poffs, rb, act, s);
+}
+
+cudaError_t launch_w8_act_scatter(const uint16_t* x, int T, int H, int Kp, int k, const int* inv, int rb, int8_t* act, float* s,
+                                  cudaStream_t stream) {
     if (T == 0) return cudaSuccess;
     // 3000 tokens of 1024 values to 4 places each: 14 us with a warp per token, 20 us with a CTA
-    if (w8 && H <= 1024)
+    if (H <= 1024)
         return launch_pdl(H <= 512 ? act_scatter_short_kernel<1> : act_scatter_short_kernel<2>, ceil_div(T, 8), 256, 0, stream, x,
                           T, H, Kp, k, inv, rb, act, s);
-    if (w8) return launch_pdl(act_scatter_w8_kernel, T, 256, 0, stream, x, H, Kp, k, inv, rb, act, s);
-    return launch_pdl(act_scatter_kernel, T + E, 128, 0, stream, x, T, H, Kp, k, inv, offs, poffs, rb, act, s);
+    return launch_pdl(act_scatter_w8_kernel, T, 256, 0, stream, x, H, Kp, k, inv, rb, act, s);
 }
 
 cudaError_t launch_w8_prepare(const int32_t* ids, const uint16_t* x, int T, int H, int Kp, int k, int E, int tile_tokens,
@@ -1267,29 +1281,41 @@ cudaError_t launch_w8_prepare(const int32_t* ids, const uint16_t* x, int T, int 
 }
 
 cudaError_t launch_requant(const uint16_t* h, int ldh, int F, int Kp, const int* row_src, const int* poffs, int E,
-                           int rows_cap, int rb, int8_t* act, float* s, cudaStream_t stream, bool w8) {
+                           int rows_cap, int rb, int8_t* act, float* s, cudaStream_t stream) {
+    if (rows_cap == 0) return cudaSuccess;
+    return launch_pdl(F <= 128 * 16 ? requant_kernel<1, false> : requant_kernel<kRowCache, false>, rows_cap, 128, 0, stream, h,
+                      ldh, F, Kp, row_src, poffs, E, rb, act, s);
+}
+
+cudaError_t launch_w8_requant(const uint16_t* h, int ldh, int F, int Kp, const int* row_src, const int* poffs, int E,
+                              int rows_cap, int rb, int8_t* act, float* s, cudaStream_t stream) {
     if (rows_cap == 0) return cudaSuccess;
     // A warp per row up to F = 2048, unless a CTA per row fits the GPU at once and a row keeps
     // most of a CTA busy (F > 1024). CTA against warp at F = 1408: 384 rows 8.7 against 10.7 us,
     // 1536 rows 10.7 both, 3840 rows 14.6 against 12.8, 49152 rows (F = 1536) 140 against 84; at
     // F = 2048: 1920 rows 11.1 against 12.9, 3840 rows 14.8 against 14.7; at F = 1024, 160 rows
     // of 512 experts 10.8 against 8.8.
-    if (w8 && F <= 2048 && (F <= 1024 || rows_cap > 16 * sm_count()))
+    if (F <= 2048 && (F <= 1024 || rows_cap > 16 * sm_count()))
         return launch_pdl(F <= 512    ? requant_short_kernel<1>
                           : F <= 1024 ? requant_short_kernel<2>
                                       : requant_short_kernel<4>,
                           ceil_div(rows_cap, 8), 256, 0, stream, h, ldh, F, Kp, row_src, poffs, E, rb, act, s);
-    const auto kernel = F <= 128 * 16 ? (w8 ? requant_kernel<1, true> : requant_kernel<1, false>)
-                                      : (w8 ? requant_kernel<kRowCache, true> : requant_kernel<kRowCache, false>);
-    return launch_pdl(kernel, rows_cap, 128, 0, stream, h, ldh, F, Kp, row_src, poffs, E, rb, act, s);
+    return launch_pdl(F <= 128 * 16 ? requant_kernel<1, true> : requant_kernel<kRowCache, true>, rows_cap, 128, 0, stream, h, ldh,
+                      F, Kp, row_src, poffs, E, rb, act, s);
 }
 
 cudaError_t launch_combine(const float* y2, int H, const int* inv, const float* w, int T, int k, uint16_t* out,
-                           cudaStream_t stream, bool w8) {
+                           cudaStream_t stream) {
     if (T == 0) return cudaSuccess;
-    // W8A8: few tokens are spread over several CTAs each
-    const dim3 grid(T, w8 && T < 2 * sm_count() ? ceil_div(H, 256 * 8) : 1);
-    return launch_pdl(w8 ? combine_kernel<true> : combine_kernel<false>, grid, 256, 0, stream, y2, H, inv, w, T, k, out);
+    return launch_pdl(combine_kernel<false>, T, 256, 0, stream, y2, H, inv, w, T, k, out);
+}
+
+cudaError_t launch_w8_combine(const float* y2, int H, const int* inv, const float* w, int T, int k, uint16_t* out,
+                              cudaStream_t stream) {
+    if (T == 0) return cudaSuccess;
+    // few tokens are spread over several CTAs each
+    const dim3 grid(T, T < 2 * sm_count() ? ceil_div(H, 256 * 8) : 1);
+    return launch_pdl(combine_kernel<true>, grid, 256, 0, stream, y2, H, inv, w, T, k, out);
 }
 
 cudaError_t launch_dense_prep(const int8_t* qa, int M, int Kq, int Kp, int tile_tokens, int rb, int8_t* act, int4* mt_tab,

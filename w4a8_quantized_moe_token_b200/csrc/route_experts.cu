@@ -20,6 +20,7 @@
 #include <type_traits>
 
 #include "../../include/w4a8.h"
+#include "layer_internal.h"
 #include "w4a8_common.cuh"
 #include "w4a8_internal.h"
 

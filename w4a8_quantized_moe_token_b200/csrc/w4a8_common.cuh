@@ -365,11 +365,6 @@ __device__ __forceinline__ bool named_bar_or(int id, int nthreads, bool pred) {
 // ---------------------------------------------------------------------------
 __device__ __forceinline__ void grid_dep_wait() { asm volatile("griddepcontrol.wait;" ::: "memory"); }
 
-// Lets the next kernel of the stream start its set-up once every CTA of this grid has come
-// here.  A kernel that allocates tensor memory calls it only after its allocation: a later
-// kernel, which waits for this one, must not be able to take the columns first.
-__device__ __forceinline__ void grid_dep_launch() { asm volatile("griddepcontrol.launch_dependents;" ::: "memory"); }
-
 template <typename... KArgs, typename... Args>
 inline cudaError_t launch_pdl(void (*kernel)(KArgs...), dim3 grid, dim3 block, size_t smem, cudaStream_t stream,
                               Args... args) {
@@ -392,9 +387,6 @@ __device__ __forceinline__ uint16_t bf16_bits(float v) { return __bfloat16_as_us
 // ---------------------------------------------------------------------------
 // quantisation arithmetic (IEEE fp32, round half to even, no contraction)
 // ---------------------------------------------------------------------------
-// the W8A8 scheme's scales are max|v| * (1 / 127), the constant and the product in fp32
-constexpr float kInv127 = 1.0f / 127.0f;
-
 // symmetric INT8 of one value with scale s > 0
 __device__ __forceinline__ int quant_i8(float x, float s) {
     float r = rintf(__fdiv_rn(x, s));

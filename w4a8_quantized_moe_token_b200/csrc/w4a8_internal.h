@@ -43,39 +43,6 @@ struct DebugInject {
     long long wait_limit = 0;
 };
 
-// the hook's current values on the calling host thread (wait_limit: the default if unset)
-long long debug_wait_limit();
-uint32_t debug_flags();
-
-// multiprocessors of the current device
-int sm_count();
-
-// records an event pair around the kernels launched in its scope while the per-kernel
-// timing (w4a8_profile_start) is on
-struct ProfScope {
-    int kind, nlaunch;
-    cudaStream_t st;
-    cudaEvent_t a = nullptr;
-    ProfScope(int kind, int nlaunch, cudaStream_t st);
-    ~ProfScope();
-};
-
-// Workspace of w4a8_moe_forward: regions in the order of the enum below.
-enum Region {
-    R_ERR, R_CHIST, R_COUNTS, R_OFFS, R_POFFS, R_MTSTART, R_MTTAB, R_PERM, R_INV, R_ROWSRC,
-    R_ACT1, R_S1, R_H, R_ACT2, R_S2, R_Y2,
-    R_XIN, R_IDSIN, R_WIN, R_OUT, R_LOGITS,  // host-buffer variants only
-    R_COUNT
-};
-
-struct MoeLayout {
-    size_t off[R_COUNT + 1];
-    size_t bytes[R_COUNT];
-    int nslots, nchunk, R, Hp, Fp, G1, G2;
-};
-// false for a shape outside the layer's limits
-bool moe_layout(int T, int E, int k, int H, int F, bool host_io, MoeLayout* L, bool w4a16 = false, int group = 128);
-
 // launchers (all asynchronous on `stream`); return the cudaGetLastError() of the launch
 // Tokens per GEMM tile (16: decode kernel, 128: wide-tile kernel) for a given mean
 // number of tokens per expert; the permutation's row-tile table must be built with
@@ -96,36 +63,22 @@ cudaError_t launch_quant_act(const uint16_t* x, int T, int K, int8_t* q, float* 
 cudaError_t launch_route_topk(const uint16_t* logits, int T, int E, int k, int32_t* ids, float* w,
                               cudaStream_t stream);
 
-cudaError_t launch_route_experts(const void* logits, int type, int T, int E, int k, int flags, const float* bias, int n_group,
-                                 int topk_group, float scale, int32_t* ids, float* w, cudaStream_t stream);
-
 // MoE pipeline pieces
-constexpr int kPermChunk = 256;       // slots per permutation chunk (multi-CTA path)
-constexpr int kPermSmallSlots = 16384;  // up to this many slots the permutation runs in one CTA
-int perm_launch_count(int nslots, int small_slots = kPermSmallSlots);
 cudaError_t launch_perm(const int32_t* ids, int nslots, int E, int tile_tokens, int* chist, int nchunk, int* counts,
                         int* offs, int* poffs, int* mtstart, int4* mt_tab, int* perm, int* inv, int* row_src,
-                        uint32_t* err, cudaStream_t stream, int small_slots = kPermSmallSlots);
+                        uint32_t* err, cudaStream_t stream);
 // capacity of the row-tile table for a layer: sum over experts of ceil(count / tile)
 // <= nslots / tile + E, with tiles of at least 16 rows
 inline int mt_tab_capacity(int nslots, int E) { return nslots / 16 + E + 1; }
 // Kp: the padded row length of the tiled rows (a multiple of 128, >= H)
-// w8: row scales as the W8A8 scheme defines them (a product with 1/127)
 cudaError_t launch_act_scatter(const uint16_t* x, int T, int H, int Kp, int k, const int* inv, const int* offs,
-                               const int* poffs, int E, int rb, int8_t* act, float* s, cudaStream_t stream,
-                               bool w8 = false);
+                               const int* poffs, int E, int rb, int8_t* act, float* s, cudaStream_t stream);
 // h: bf16 SwiGLU output rows of ldh values
 cudaError_t launch_requant(const uint16_t* h, int ldh, int F, int Kp, const int* row_src, const int* poffs, int E,
-                           int rows_cap, int rb, int8_t* act, float* s, cudaStream_t stream, bool w8 = false);
-// W8A8 layer, T * k <= kPrepareSlots: launch_perm and launch_act_scatter (w8) in one kernel,
-// which also sets the error word
-constexpr int kPrepareSlots = 2048;
-cudaError_t launch_w8_prepare(const int32_t* ids, const uint16_t* x, int T, int H, int Kp, int k, int E, int tile_tokens,
-                              int* counts, int* offs, int* poffs, int* mtstart, int4* mt_tab, int* perm, int* inv, int* row_src,
-                              int rb, int8_t* act, float* s, uint32_t* err, cudaStream_t stream);
+                           int rows_cap, int rb, int8_t* act, float* s, cudaStream_t stream);
 // y2: fp32 expert outputs [rows][H]
 cudaError_t launch_combine(const float* y2, int H, const int* inv, const float* w, int T, int k, uint16_t* out,
-                           cudaStream_t stream, bool w8 = false);
+                           cudaStream_t stream);
 // qa rows of Kq columns into tiled rows of Kp >= Kq columns (the rest zero)
 cudaError_t launch_dense_prep(const int8_t* qa, int M, int Kq, int Kp, int tile_tokens, int rb, int8_t* act, int4* mt_tab,
                               int* n_mtiles, cudaStream_t stream);
@@ -139,6 +92,9 @@ cudaError_t launch_dense_prep_bf16(const uint16_t* x, int M, int K, uint8_t* act
 cudaError_t launch_act_gather_bf16(const uint16_t* x, int T, int H, int k, const int* inv, uint8_t* x16, uint8_t* h16,
                                    int F, cudaStream_t stream);
 
+constexpr int kPermChunk = 256;       // slots per permutation chunk (multi-CTA path)
+constexpr int kPermSmallSlots = 16384;  // up to this many slots the permutation runs in one CTA
+int perm_launch_count(int nslots);
 
 // INT8 KV cache (kv_int8.cu)
 int kv_max_heads();

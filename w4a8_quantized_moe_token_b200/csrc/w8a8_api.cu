@@ -1,8 +1,8 @@
 // C ABI of the W8A8 scheme (declarations and contract: include/w8a8.h): argument
 // validation, workspace carve-up and launch sequences.
 #include "../../include/w8a8.h"
+#include "layer_internal.h"
 #include "w4a8_common.cuh"
-#include "w4a8_internal.h"
 #include "w8a8_internal.h"
 
 #define W4A8_EXPORT extern "C" __attribute__((visibility("default")))
@@ -179,7 +179,7 @@ W4A8_EXPORT int w8a8_moe_forward(const void* packed_up, const void* packed_down,
                                poffs, mtstart, at<int4>(ws, L, R_MTTAB), at<int>(ws, L, R_PERM), inv, row_src, err, st, kPrepareSlots));
         }
         ProfScope p(W4A8_KERNEL_ACT_QUANT, 1, st);
-        W8_TRY(launch_act_scatter(x, T, H, L.Hp, k, inv, offs, poffs, E, L.R, act1, s1, st, true));
+        W8_TRY(launch_w8_act_scatter(x, T, H, L.Hp, k, inv, L.R, act1, s1, st));
     }
     W8Args a{};
     W8Operands op{};
@@ -207,7 +207,7 @@ W4A8_EXPORT int w8a8_moe_forward(const void* packed_up, const void* packed_down,
     }
     {
         ProfScope p(W4A8_KERNEL_REQUANT, 1, st);
-        W8_TRY(launch_requant(h, L.Fp, F, L.Fp, row_src, poffs, E, L.R, L.R, act2, s2, st, true));
+        W8_TRY(launch_w8_requant(h, L.Fp, F, L.Fp, row_src, poffs, E, L.R, L.R, act2, s2, st));
     }
     a.NT = w8_tiles(H, W4A8_LAYOUT_PLAIN);
     a.G = L.Fp / kGroup;
@@ -226,7 +226,7 @@ W4A8_EXPORT int w8a8_moe_forward(const void* packed_up, const void* packed_down,
     }
     {
         ProfScope p(W4A8_KERNEL_COMBINE, 1, st);
-        W8_TRY(launch_combine(y2, H, inv, w, T, k, static_cast<uint16_t*>(out_bf16), st, true));
+        W8_TRY(launch_w8_combine(y2, H, inv, w, T, k, static_cast<uint16_t*>(out_bf16), st));
     }
     return W4A8_OK;
 }
