@@ -14,8 +14,8 @@
  *
  * The conventions of w4a8.h hold for every entry point here: caller-owned device memory,
  * caller's workspace and stream, argument errors as a w4a8_status, device errors in the
- * workspace (w8a8_gemm_last_error, and w4a8_last_device_error for the layer), nothing allocated.  Serving only: no
- * backward pass.
+ * workspace (w8a8_gemm_last_error, and w4a8_last_device_error for the layer), nothing
+ * allocated.  Serving only: no backward pass.
  */
 #ifndef W8A8_H
 #define W8A8_H

@@ -15,6 +15,10 @@
 // the next one, or at the border of the kept groups, is done again in 64 bits (about one row
 // in a few hundred for random inputs): exact order at the price of fp32 arithmetic.  Without
 // a bias the keys are the logits themselves and nothing is ever in doubt.
+//
+// Bound by instruction issue, not by memory: 16384 x 384 fp32 logits (sigmoid, bias, 4 of 8
+// groups) take 31-33 us on B200, 1477 warp instructions per token, for 4 us of bytes; one
+// token 4.8 us, 64 x 64 (softmax) 3.4 us, both in a graph.
 #include <math_constants.h>
 
 #include <type_traits>
