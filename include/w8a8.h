@@ -52,7 +52,8 @@ int w8a8_pack_weights(const void* w_bf16, int E, int N, int K, int layout, void*
 
 /* One dense W8A8 linear layer:
  *   y[m][n] = sa[m] * sw[n] * sum_k qa[m][k] * qw[n][k] (+ bias[n]),
- * the sum exact in INT32, the rest fp32, rounded once to the output type.
+ * the sum exact in INT32, the rest fp32 (the sum times sa, times sw, plus the bias, in this
+ * order), rounded once to the output type.
  *   qa       : device int8 [M][Kp], Kp = K rounded up to 128, padding 0 (as w4a8_quant_act
  *              writes it), 16-byte aligned.
  *   sa       : device float [M] (may be NULL for W8A8_I32).
@@ -73,8 +74,8 @@ int w8a8_gemm_last_error(const void* ws, void* stream);
 /* The MoE expert FFN with W8A8 experts: the arguments, routing, permutation, activation
  * quantisation and combine of w4a8_moe_forward,
  *   out[t] = sum_j w[t][j] * Down_e(SwiGLU(Up_e(x[t]))),  e = ids[t][j],
- * h = silu(gate) * up rounded to bf16 and requantised per token before Down, the experts'
- * outputs summed in fp32, j ascending, and rounded once to bf16.  An id out of range drops
+ * h = silu(gate) * up (fp32, within 7 roundings) rounded to bf16 and requantised per token
+ * before Down, the experts' outputs summed in fp32, j ascending, and rounded once to bf16.  An id out of range drops
  * its slot and sets bit 1 of the error word.
  *   packed_up   : from w8a8_pack_weights(E, 2F, H, W4A8_LAYOUT_GATEUP).
  *   packed_down : from w8a8_pack_weights(E, H, F, W4A8_LAYOUT_PLAIN).

@@ -1,5 +1,5 @@
 """GPU parity of the W8A8 epilogues on inputs whose INT32 sums and scales are exact in fp32, so
-that the roundings left can be counted one by one."""
+that the roundings left can be counted one by one, and at scales far from 1."""
 
 import numpy as np
 import pytest
@@ -7,7 +7,7 @@ import torch
 
 from oracle import w4a8_oracle as O
 from oracle import w8a8_oracle as W
-from test_gpu_w8a8 import dev_bf16, pack
+from test_gpu_w8a8 import HALF_STEP, TINY, dev_bf16, pack, run_gemm
 from w4a8_quantized_moe_token_b200 import binding as B
 from w4a8_quantized_moe_token_b200 import synth
 
@@ -49,3 +49,28 @@ def test_swiglu_rounds_the_64_bit_value(T, F):
     lo, hi = (O.round_to_bf16((ref + s * fp32).astype(np.float64)) for s in (-1, 1))
     bad = (h < lo) | (h > hi)
     assert not bad.any(), f"{int(bad.sum())} of {bad.size}, at g = {g[bad][:5]}: {h[bad][:5]} and not {ref[bad][:5]}"
+
+
+@pytest.mark.parametrize("dtype", [torch.float32, torch.bfloat16, torch.float16])
+@pytest.mark.parametrize("M,N,K", [(3, 64, 512), (5, 257, 300), (300, 514, 640), (40, 512, 4096)])
+def test_gemm_scales_whose_product_fp32_does_not_hold(dtype, M, N, K):
+    """A token's and a channel's scale of about 2^-67 multiply to less than fp32's smallest
+    normal value, while the outputs, 2^-134 times sums of about 2^15, lie above it but for the
+    smallest sums; in rows with a scale of 2^100 a sum of 0 stays 0 where the scales' product is
+    infinite.  Roundings as counted elsewhere, and one more: below 2^-126 the last product is
+    rounded to a multiple of 2^-149, by at most 2^-150."""
+    rng = np.random.default_rng([M, N, K])
+    qa, sa = O.quantize_act(synth.normal_bf16(rng, (M, K)))
+    w = synth.normal_bf16(rng, (N, K), 2.0 ** -62)
+    w[1::2] *= 2.0 ** 105  # even channels: scales of about 2^-67, odd ones: 2^38
+    qa[2::3] = 0
+    sa = (sa * 2.0 ** -61).astype(np.float32)
+    sa[2::3] = 2.0 ** 100
+    qw, sw = W.quantize(w)
+    product = np.outer(sa.astype(np.float64), sw)
+    assert (product[0, ::2] < 2.0 ** -126).all() and (product[2, 1::2] > 3.5e38).all()
+    got = run_gemm(qa, sa, pack(w), N, K, dtype).double().numpy()
+    ref = W.linear(qa, sa, qw, sw)
+    bound = W.linear_error_bound(qa, sa, qw, sw) + 2.0 ** -150
+    bound = bound + HALF_STEP[dtype] * (np.abs(ref) + bound) + TINY[dtype]
+    assert np.all(np.abs(got - ref) <= bound), f"{int((np.abs(got - ref) > bound).sum())} of {ref.size} outside"

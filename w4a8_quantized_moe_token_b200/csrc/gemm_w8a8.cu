@@ -255,6 +255,11 @@ __device__ __forceinline__ float w8_silu_mul(float g, float u) {
     return __fmaf_rn(__fmaf_rn(-q, d, n), r, q) * u;
 }
 
+// A sum with the token's and the channel's scale, one after the other: |sum| >= 1, or 0, so that
+// small scales cost no bits before the last product (the scales' own product may lie below
+// fp32's range, or above it, where the result does not)
+__device__ __forceinline__ float scaled(uint32_t sum, float sa, float sw) { return __int2float_rn((int)sum) * sa * sw; }
+
 // Output kinds of the epilogue.  kOutPair: 16-bit rows that may be stored two columns at a time.
 enum { kOutF32, kOutI32, kOutBf16, kOutF16, kOutPairBf16, kOutPairF16, kOutSwiglu };
 
@@ -292,7 +297,7 @@ __device__ __forceinline__ void w8_store(const uint32_t (&v)[16], float sw, floa
     if (kOut == kOutF32 || kOut == kOutI32 || kOut == kOutBf16 || kOut == kOutF16) {
 #pragma unroll
         for (int i = 0; i < 16; ++i, out += pitch) {
-            const float y = kOut == kOutI32 ? 0.f : __int2float_rn((int)v[i]) * (sw * s[i]) + bias;
+            const float y = kOut == kOutI32 ? 0.f : scaled(v[i], s[i], sw) + bias;
             const bool p = valid && i < ncol;
             if (kOut == kOutF32) st_if(p, out, __float_as_uint(y));
             else if (kOut == kOutI32) st_if(p, out, v[i]);
@@ -304,8 +309,8 @@ __device__ __forceinline__ void w8_store(const uint32_t (&v)[16], float sw, floa
         float own[8], recv[8];
 #pragma unroll
         for (int i = 0; i < 16; i += 2) {
-            const float p0 = __int2float_rn((int)v[i]) * (sw * s[i]) + bias;
-            const float p1 = __int2float_rn((int)v[i + 1]) * (sw * s[i + 1]) + bias;
+            const float p0 = scaled(v[i], s[i], sw) + bias;
+            const float p1 = scaled(v[i + 1], s[i + 1], sw) + bias;
             own[i / 2] = odd ? p1 : p0;
             recv[i / 2] = __shfl_xor_sync(0xffffffffu, odd ? p0 : p1, 1);
         }
@@ -322,10 +327,9 @@ __device__ __forceinline__ void w8_store(const uint32_t (&v)[16], float sw, floa
         float own[8], recv[8];
 #pragma unroll
         for (int i = 0; i < 16; i += 2) {
-            const float p0 = __int2float_rn((int)v[i]) * sw, p1 = __int2float_rn((int)v[i + 1]) * sw;
-            const float si = odd ? s[i + 1] : s[i];
-            own[i / 2] = (odd ? p1 : p0) * si;
-            recv[i / 2] = __shfl_xor_sync(0xffffffffu, odd ? p0 : p1, 1) * si;
+            const float p0 = scaled(v[i], s[i], sw), p1 = scaled(v[i + 1], s[i + 1], sw);
+            own[i / 2] = odd ? p1 : p0;
+            recv[i / 2] = __shfl_xor_sync(0xffffffffu, odd ? p0 : p1, 1);
         }
         uint16_t h[8];
 #pragma unroll
@@ -587,7 +591,7 @@ __global__ void __launch_bounds__(kW8Threads, 1)
                     for (int k = 0; k < 4; ++k) {
                         const size_t at = (size_t)(t.row0 + first + i + k) * a.ldo + n;
                         if (n < a.nvalid && i + k < count) {
-                            const float y = __int2float_rn(sums[k]) * (sw * sa_s[i + k]) + bias;
+                            const float y = scaled((uint32_t)sums[k], sa_s[i + k], sw) + bias;
                             if (a.out_kind == kOutI32) static_cast<int32_t*>(a.out)[at] = sums[k];
                             else if (a.out_kind == kOutF32) static_cast<float*>(a.out)[at] = y;
                             else if (a.out_kind == kOutF16 || a.out_kind == kOutPairF16)
