@@ -311,10 +311,16 @@ __global__ void __launch_bounds__(kRouteWarps * 32, kPL <= 12 ? 12 : kPL <= 16 ?
         }
         bool keep = g < a.n_group && beaten < a.topk_group;
         if (!by_logit && a.topk_group < a.n_group) {
-            // the worst group kept against the best one left out
-            const float lo = value_of(__reduce_min_sync(kAll, keep ? key_of(gs) : kAll));
-            const float hi = value_of(__reduce_max_sync(kAll, g < a.n_group && !keep ? key_of(gs) : 0x007FFFFFu));
-            if (hi > -CUDART_INF_F && !(lo - hi > 4.0f * delta + 4.76837158e-07f * (fabsf(lo) + fabsf(hi)))) {
+            // Error of a group's score: of its one or two values delta and 2^-24 of the value each,
+            // of their sum 2^-24 of it; together below 2 delta + 2^-23 of the values' magnitudes,
+            // which may be far above a sum that cancels.  Twice the second part covers the bounds'
+            // own roundings.  The worst group kept, at its lowest, against the best one left out,
+            // at its highest (a masked group is exact; an infinite one is always in doubt).
+            const float size = fabsf(b0) + (top2 && b1 > -CUDART_INF_F ? fabsf(b1) : 0.f);
+            const float err = b0 > -CUDART_INF_F ? 2.0f * delta + 2.38418579e-07f * size : 0.f;
+            const float lo = value_of(__reduce_min_sync(kAll, keep ? key_of(fmaxf(gs - err, -CUDART_INF_F)) : kAll));
+            const float hi = value_of(__reduce_max_sync(kAll, g < a.n_group && !keep ? key_of(gs + err) : 0x007FFFFFu));
+            if (hi > -CUDART_INF_F && !(lo > hi)) {
                 const double gs64 = group_score64<T>(a, x, sm64, top, lpg);
                 beaten = 0;
                 for (int q = 0; q < a.n_group; ++q) {
