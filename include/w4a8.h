@@ -152,7 +152,10 @@ int w4a8_route_topk(const void* logits_bf16, int T, int E, int k, int32_t* ids, 
  *   ids[t]= the k largest c of the eligible experts, largest first, ties to the lower id;
  *   w[t][j] = s[ids[t][j]], with W4A8_ROUTE_RENORM divided by their sum (which the chosen
  *           logits alone determine: no underflow of the scores enters), times `scale`.
- * Scores are compared as 64-bit values, so that ids do not depend on fp32 rounding.
+ * Scores are compared as 64-bit values, so that ids do not depend on fp32 rounding.  The
+ * weights are fp32: off by less than 2^-18 of their value in the worst case (64 roundings of
+ * exponentials, a sum over up to 1024 experts, quotient and factor), where that is a normal
+ * number; a few 2^-24 as a rule.
  * An expert whose logit is -inf or NaN, or whose bias is, is masked: it ranks after every
  * other one (ties to the lower id), adds nothing to its group's score and, should it fill a
  * row that has fewer than k others, has weight 0; a row with nothing unmasked has all

@@ -1,4 +1,5 @@
-"""w4a8_route_experts where 32 bits do not decide the order of the groups."""
+"""w4a8_route_experts where 32 bits do not decide the order of the groups, and where logits lie
+far apart."""
 
 import pytest
 import torch
@@ -32,3 +33,20 @@ def test_groups_under_large_biases_of_opposite_sign(sigmoid, E, n_group, topk_gr
     x = logits_of(E, T, E, "fp32")
     check(x, k, sigmoid, top2=True, bias=bias.reshape(-1), n_group=n_group, topk_group=topk_group)
     check(x, k, sigmoid, top2=False, bias=bias.reshape(-1), n_group=n_group, topk_group=topk_group)
+
+
+@pytest.mark.parametrize("dtype", ["bf16", "fp16", "fp32"])
+@pytest.mark.parametrize("std", [3.0, 10.0, 30.0])
+@pytest.mark.parametrize("renorm", [False, True])
+def test_weights_of_logits_far_below_the_largest(dtype, std, renorm):
+    """The 8 chosen logits lie tens below the row's largest one: the difference from it, 30 or
+    so, is rounded to 2^-19 by a 32-bit subtraction, and its exponential by as much."""
+    for E in (12, 64, 384):
+        check(logits_of(E, 300, E, dtype, std), 8, renorm=renorm)
+        check(logits_of(E, 300, E, dtype, std), 8, sigmoid=True, renorm=renorm)
+    x = logits_of(5, 300, 64, dtype, 1.0)
+    x[:, :9] = logits_of(6, 300, 9, dtype, std) - 20.0
+    bias = torch.zeros(64)
+    bias[:9] = 5.0  # chosen for their bias, weighted without it
+    check(x, 9, renorm=renorm, bias=bias)
+    check(x, 9, sigmoid=True, renorm=renorm, bias=bias)

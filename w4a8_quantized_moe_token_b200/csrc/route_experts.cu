@@ -462,7 +462,12 @@ __global__ void __launch_bounds__(kRouteWarps * 32, kPL <= 12 ? 12 : kPL <= 16 ?
     const float ex = sigmoid ? fminf(xv, 0.f) : xv;
     float ref = sigmoid ? 0.f : top;
     if (renorm) ref = value_of(__reduce_max_sync(kAll, live ? key_of(ex) : 0x007FFFFFu));
-    float s = live ? expf(ex == ref ? 0.f : ex - ref) : 0.f;
+    // A difference of tens is rounded by some 2^-19, and its exponential by as much of itself:
+    // what the subtraction lost (exact, the two-sum's second half) corrects it.
+    const float d = ex == ref ? 0.f : ex - ref, v0 = d - ex;
+    const float lost = ex == ref ? 0.f : (ex - (d - v0)) - (ref + v0);
+    float s = live ? expf(d) : 0.f;
+    if (s > 0.f) s = __fmaf_rn(s, lost, s);  // (0: too far below, or beside an infinite one)
     if (live && sigmoid) s = __fdiv_rn(s, 1.0f + expf(-fabsf(xv)));
     if (renorm) {
         float total = s;
