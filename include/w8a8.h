@@ -9,8 +9,11 @@
  * primer (hotelren.com 5982361, section 2.1):
  *       s = max|v| * (1 / 127) (constant and product in fp32),
  *       q = clamp(round(v / s), -127, 127) (correctly rounded fp32 quotient),
- * round half to even; an all-zero row has s = 0 and q = 0.  (w4a8_quant_act divides by 127
- * instead: its scales may be one fp32 step away; w8a8_gemm takes any codes and scales.)
+ * round half to even; an all-zero row has s = 0 and q = 0.  A row with a NaN has s = NaN, one
+ * with an infinity and no NaN s = infinity, both q = 0: a channel of weights, a token or a row
+ * of h that holds one makes every output that it enters NaN (W8A8_I32 sums: 0).
+ * (w4a8_quant_act divides by 127 instead, so that its scales may be one fp32 step away, and
+ * passes over NaN; w8a8_gemm takes any codes and scales.)
  *
  * The conventions of w4a8.h hold for every entry point here: caller-owned device memory,
  * caller's workspace and stream, argument errors as a w4a8_status, device errors in the

@@ -714,21 +714,22 @@ __global__ void __launch_bounds__(256) pack_w8_kernel(const uint16_t* __restrict
             for (int i = 0; i < 16; ++i) v[i] = k0 + i < K ? __uint_as_float((uint32_t)row[k0 + i] << 16) : 0.f;
         }
     };
-    float amax = 0.f;
+    // the largest magnitude by its bits: a NaN is above infinity, and either becomes the scale,
+    // with codes 0 (all outputs of the channel are 0 times it: NaN)
+    uint32_t bits = 0u;
     if (valid) {
         for (int ci = lane; ci < G * 8; ci += 32) {
             load16(ci * 16);
 #pragma unroll
-            for (int i = 0; i < 16; ++i) amax = fmaxf(amax, fabsf(v[i]));
+            for (int i = 0; i < 16; ++i) bits = max(bits, __float_as_uint(fabsf(v[i])));
         }
     }
-#pragma unroll
-    for (int o = 16; o > 0; o >>= 1) amax = fmaxf(amax, __shfl_xor_sync(0xffffffffu, amax, o));
+    const float amax = __uint_as_float(__reduce_max_sync(0xffffffffu, bits));
     const float sc = __fmul_rn(amax, kInv127);
     const float rinv = __fdiv_rn(1.0f, sc);
     for (int ci = lane; ci < G * 8; ci += 32) {
         uint32_t out[4] = {0u, 0u, 0u, 0u};
-        if (valid && amax > 0.f) {
+        if (valid && amax > 0.f && amax < INFINITY) {
             load16(ci * 16);
 #pragma unroll
             for (int i = 0; i < 16; ++i) out[i >> 2] |= (uint32_t)(quant_i8_fast(v[i], sc, rinv) & 0xFF) << (8 * (i & 3));

@@ -570,6 +570,14 @@ __device__ __forceinline__ float row_scale(float amax) {
     return kW8 ? __fmul_rn(amax, kInv127) : __fdiv_rn(amax, 127.0f);
 }
 
+// the larger of amax and |v|: NaN are passed over, or (W8A8) larger than everything, as the
+// magnitudes' bits order them
+template <bool kW8>
+__device__ __forceinline__ float larger(float amax, float v) {
+    if (kW8) return __uint_as_float(max(__float_as_uint(amax), __float_as_uint(fabsf(v))));
+    return fmaxf(amax, fabsf(v));
+}
+
 template <int kCache, bool kW8, typename TIn>
 __device__ __forceinline__ void quant_row_cta(const TIn* row, int len, int Kp, int r, int RB,
                                               int8_t* __restrict__ act, float* __restrict__ s) {
@@ -586,25 +594,25 @@ __device__ __forceinline__ void quant_row_cta(const TIn* row, int len, int Kp, i
             if (ci < nch) {
                 load_chunk(row, len, ci * 16, cache[c], kW8);
 #pragma unroll
-                for (int i = 0; i < 16; ++i) amax = fmaxf(amax, fabsf(cache[c].v[i]));
+                for (int i = 0; i < 16; ++i) amax = larger<kW8>(amax, cache[c].v[i]);
             }
         }
         for (int ci = t + kCache * 128; ci < nch; ci += 128) {
             Chunk16 tmp;
             load_chunk(row, len, ci * 16, tmp, kW8);
 #pragma unroll
-            for (int i = 0; i < 16; ++i) amax = fmaxf(amax, fabsf(tmp.v[i]));
+            for (int i = 0; i < 16; ++i) amax = larger<kW8>(amax, tmp.v[i]);
         }
     }
-    amax = warp_max(amax);
+    amax = kW8 ? __uint_as_float(__reduce_max_sync(0xffffffffu, __float_as_uint(amax))) : warp_max(amax);
     if ((t & 31) == 0) red[t >> 5] = amax;
     __syncthreads();
-    amax = fmaxf(fmaxf(red[0], red[1]), fmaxf(red[2], red[3]));
+    amax = larger<kW8>(larger<kW8>(red[0], red[1]), larger<kW8>(red[2], red[3]));
     const float sc = row_scale<kW8>(amax);
     const float rinv = __fdiv_rn(1.0f, sc);
     auto emit = [&](int ci, const Chunk16& c) {
         uint32_t out[4] = {0u, 0u, 0u, 0u};
-        if (amax > 0.f) {
+        if (amax > 0.f && (!kW8 || amax < INFINITY)) {
 #pragma unroll
             for (int i = 0; i < 16; ++i) {
                 const uint32_t q = (uint32_t)(quant_i8_fast(c.v[i], sc, rinv) & 0xFF);
@@ -753,13 +761,17 @@ __device__ __forceinline__ void load_raw(const uint16_t* row, int len, int k0, b
     }
 }
 
-// the larger of amax and the chunk's magnitudes (NaN are passed over)
-__device__ __forceinline__ float raw_amax(const Raw16& c, float amax) {
+// The largest magnitude of a row as bf16 bits, which order magnitudes, infinity above them and
+// NaN above that: the row's scale tells of either (`m`: two maxima side by side).
+__device__ __forceinline__ uint32_t raw_max(const Raw16& c, uint32_t m) {
 #pragma unroll
-    for (int i = 0; i < 8; ++i)
-        amax = fmaxf(amax, fmaxf(fabsf(__uint_as_float(c.w[i] << 16)), fabsf(__uint_as_float(c.w[i] & 0xFFFF0000u))));
-    return amax;
+    for (int i = 0; i < 8; ++i) m = __vmaxu2(m, c.w[i] & 0x7FFF7FFFu);
+    return m;
 }
+__device__ __forceinline__ uint32_t warp_max_raw(uint32_t m) { return __reduce_max_sync(0xffffffffu, max(m >> 16, m & 0xFFFFu)); }
+// Rows with a NaN or an infinity, and rows of zeros, have codes 0; with the first two's scale
+// every output that they enter is 0 * NaN or 0 * infinity.
+__device__ __forceinline__ bool raw_has_codes(uint32_t bits) { return bits > 0u && bits < 0x7F80u; }
 
 // INT8 codes of 16 values, the codes of quant_i8 bit for bit, where no |value| exceeds the
 // amax behind sc (so that nothing saturates).  t = x * inv + 1.5 * 2^23 holds rint(x * inv) in
@@ -813,23 +825,23 @@ __global__ void __launch_bounds__(256) requant_short_kernel(const uint16_t* __re
     if (!exists) return;
     const int src = row_src[r];  // (a pad row is read, not written)
     Raw16 c[kChunks];
-    float amax = 0.f;
+    uint32_t m = 0u;
 #pragma unroll
     for (int q = 0; q < kChunks; ++q)
         if (lane + 32 * q < nch) load_raw(row, F, (lane + 32 * q) * 16, true, c[q]);
     if (src < 0) return;
 #pragma unroll
     for (int q = 0; q < kChunks; ++q)
-        if (lane + 32 * q < nch) amax = raw_amax(c[q], amax);
-    amax = warp_max(amax);
-    const float sc = row_scale<true>(amax);
+        if (lane + 32 * q < nch) m = raw_max(c[q], m);
+    m = warp_max_raw(m);
+    const float sc = row_scale<true>(__uint_as_float(m << 16));
     const float rinv = __fdiv_rn(1.0f, sc);
 #pragma unroll
     for (int q = 0; q < kChunks; ++q) {
         const int ci = lane + 32 * q;
         if (ci < nch)
             *reinterpret_cast<uint4*>(act + act_offset(r, ci * 16, Kp / kGroup, RB)) =
-                amax > 0.f ? quant16(c[q], sc, rinv) : make_uint4(0u, 0u, 0u, 0u);
+                raw_has_codes(m) ? quant16(c[q], sc, rinv) : make_uint4(0u, 0u, 0u, 0u);
     }
     if (lane == 0) s[r] = sc;
 }
@@ -848,20 +860,20 @@ __global__ void __launch_bounds__(256) act_scatter_short_kernel(const uint16_t* 
     const int nch = Kp / 16, G = Kp / kGroup;
     const int my_dst = lane < k ? __ldg(inv + (size_t)tok * k + lane) : -1;
     Raw16 c[kChunks];
-    float amax = 0.f;
+    uint32_t m = 0u;
 #pragma unroll
     for (int q = 0; q < kChunks; ++q)
         if (lane + 32 * q < nch) load_raw(row, H, (lane + 32 * q) * 16, (H & 7) == 0, c[q]);
 #pragma unroll
     for (int q = 0; q < kChunks; ++q)
-        if (lane + 32 * q < nch) amax = raw_amax(c[q], amax);
-    amax = warp_max(amax);
-    const float sc = row_scale<true>(amax);
+        if (lane + 32 * q < nch) m = raw_max(c[q], m);
+    m = warp_max_raw(m);
+    const float sc = row_scale<true>(__uint_as_float(m << 16));
     const float rinv = __fdiv_rn(1.0f, sc);
 #pragma unroll
     for (int q = 0; q < kChunks; ++q) {
         const int ci = lane + 32 * q;
-        const uint4 o = ci < nch && amax > 0.f ? quant16(c[q], sc, rinv) : make_uint4(0u, 0u, 0u, 0u);
+        const uint4 o = ci < nch && raw_has_codes(m) ? quant16(c[q], sc, rinv) : make_uint4(0u, 0u, 0u, 0u);
         for (int j = 0; j < k; ++j) {
             const int r = __shfl_sync(0xffffffffu, my_dst, j);
             if (r >= 0 && ci < nch) *reinterpret_cast<uint4*>(act + act_offset(r, ci * 16, G, RB)) = o;
@@ -873,28 +885,28 @@ __global__ void __launch_bounds__(256) act_scatter_short_kernel(const uint16_t* 
 // The quantisation of one row by a CTA of 256 threads, written to the places dst[0 .. k): two
 // chunks per thread in registers (loaded by the caller), longer rows read again.
 __device__ __forceinline__ void quant_row_places(const uint16_t* row, int H, int Kp, int k, const Raw16 (&cache)[2],
-                                                 const int* dst, float* red, int RB, int8_t* __restrict__ act,
+                                                 const int* dst, uint32_t* red, int RB, int8_t* __restrict__ act,
                                                  float* __restrict__ s) {
     const int tid = threadIdx.x, nch = Kp / 16, G = Kp / kGroup;
     const bool aligned = (H & 7) == 0;
-    float amax = 0.f;
+    uint32_t m = 0u;
 #pragma unroll
     for (int c = 0; c < 2; ++c)
-        if (tid + c * 256 < nch) amax = raw_amax(cache[c], amax);
+        if (tid + c * 256 < nch) m = raw_max(cache[c], m);
     for (int ci = tid + 512; ci < nch; ci += 256) {
         Raw16 tmp;
         load_raw(row, H, ci * 16, aligned, tmp);
-        amax = raw_amax(tmp, amax);
+        m = raw_max(tmp, m);
     }
-    amax = warp_max(amax);
-    if ((tid & 31) == 0) red[tid >> 5] = amax;
+    m = warp_max_raw(m);
+    if ((tid & 31) == 0) red[tid >> 5] = m;
     __syncthreads();  // (dst, too, is complete)
 #pragma unroll
-    for (int w = 0; w < 8; ++w) amax = fmaxf(amax, red[w]);
-    const float sc = row_scale<true>(amax);
+    for (int w = 0; w < 8; ++w) m = max(m, red[w]);
+    const float sc = row_scale<true>(__uint_as_float(m << 16));
     const float rinv = __fdiv_rn(1.0f, sc);
     auto emit = [&](int ci, const Raw16& c) {
-        const uint4 q = amax > 0.f ? quant16(c, sc, rinv) : make_uint4(0u, 0u, 0u, 0u);
+        const uint4 q = raw_has_codes(m) ? quant16(c, sc, rinv) : make_uint4(0u, 0u, 0u, 0u);
         for (int j = 0; j < k; ++j)
             if (dst[j] >= 0) *reinterpret_cast<uint4*>(act + act_offset(dst[j], ci * 16, G, RB)) = q;
     };
@@ -917,7 +929,7 @@ __global__ void __launch_bounds__(256) act_scatter_w8_kernel(const uint16_t* __r
     grid_dep_launch();
     grid_dep_wait();
     __shared__ int dst[32];
-    __shared__ float red[8];
+    __shared__ uint32_t red[8];
     const int tid = threadIdx.x, nch = Kp / 16;
     const uint16_t* row = x + (size_t)blockIdx.x * H;
     Raw16 cache[2];
@@ -971,7 +983,7 @@ __global__ void __launch_bounds__(256) w8_prepare_kernel(const int32_t* __restri
     __shared__ int s_ids[kPrepareSlots];
     __shared__ int s_off[kMaxExperts], s_poff[kMaxExperts];  // counts first, then offsets
     __shared__ int sh[8], dst[32], s_bad;
-    __shared__ float red[8];
+    __shared__ uint32_t red[8];
     const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
     const int tok = blockIdx.x, nslots = T * k;
     const int nch = Kp / 16;
