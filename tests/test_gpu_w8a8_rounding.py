@@ -1,5 +1,6 @@
 """GPU parity of the W8A8 epilogues on inputs whose INT32 sums and scales are exact in fp32, so
-that the roundings left can be counted one by one, and at scales far from 1."""
+that the roundings left can be counted one by one, at scales far from 1, and at the largest
+sums."""
 
 import numpy as np
 import pytest
@@ -74,3 +75,16 @@ def test_gemm_scales_whose_product_fp32_does_not_hold(dtype, M, N, K):
     bound = W.linear_error_bound(qa, sa, qw, sw) + 2.0 ** -150
     bound = bound + HALF_STEP[dtype] * (np.abs(ref) + bound) + TINY[dtype]
     assert np.all(np.abs(got - ref) <= bound), f"{int((np.abs(got - ref) > bound).sum())} of {ref.size} outside"
+
+
+def test_gemm_largest_sums_with_codes_of_minus_128():
+    # activation codes may be -128, weights' are within +-127: 127 * 128 * 2^17 < 2^31
+    K, N = 131072, 3
+    qa = np.full((2, K), -128, np.int8)
+    qa[1, ::2] = 127
+    w = np.ones((N, K), np.float32)
+    w[1] = -1.0
+    w[2, 1::2] = -1.0
+    got = run_gemm(qa, None, pack(w), N, K, torch.int32).numpy()
+    assert np.array_equal(got, W.int_sums(qa, W.quantize(w)[0]))
+    assert np.abs(got).max() == 127 * 128 * K

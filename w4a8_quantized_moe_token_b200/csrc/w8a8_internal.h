@@ -17,7 +17,9 @@ namespace w4a8 {
 constexpr int kW8BlockBytes = kTileRows * kGroup;
 constexpr uint32_t kW8PackMagic = 0x38413857u;  // "W8A8"
 constexpr int kW8StatusWords = 1024;
-constexpr int kW8MaxK = 1 << 17;                // 2^17 products of at most 2^14 stay below 2^31
+// INT32 holds the sum of kW8MaxK products: packed weights are within +-127, activation codes
+// within -128 .. 127, so at most 127 * 128 * 2^17 = 2130706432 < 2^31
+constexpr int kW8MaxK = 1 << 17;
 inline size_t w8_blocks_offset(int E, int NT) { return (size_t)kHeaderBytes + (size_t)E * NT * kTileRows * 4; }
 inline int w8_tiles(int N, int layout) {
     return layout == W4A8_LAYOUT_GATEUP ? ceil_div(N / 2, kTileRows / 2) : ceil_div(N, kTileRows);
