@@ -1325,7 +1325,10 @@ cudaError_t launch_combine(const float* y2, int H, const int* inv, const float* 
 cudaError_t launch_w8_combine(const float* y2, int H, const int* inv, const float* w, int T, int k, uint16_t* out,
                               cudaStream_t stream) {
     if (T == 0) return cudaSuccess;
-    // few tokens are spread over several CTAs each
+    // Few tokens are spread over several CTAs each.  The layer (F 256, 4 of 32 experts) with and
+    // without: 1 token, H 7168, 33.1 and 36.7 us; 64 tokens 60.2 and 68.6, H 4096 47.9 and 51.9,
+    // H 2048 (one CTA either way) 29.4; 290 tokens, H 7168, 69.4 and 79.4.  (Beyond the rule's two
+    // CTAs per SM it would still gain: 600 tokens, H 7168, 92.6 and 102.5.)
     const dim3 grid(T, T < 2 * sm_count() ? ceil_div(H, 256 * 8) : 1);
     return launch_pdl(combine_kernel<true>, grid, 256, 0, stream, y2, H, inv, w, T, k, out);
 }
