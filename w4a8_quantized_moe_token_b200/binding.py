@@ -179,6 +179,12 @@ def _device_of_call(t, name) -> int:
     return _current_device()
 
 
+def _need_c_ints(*v):
+    """ctypes would pass the low 32 bits of a larger integer on without a word."""
+    if any(i >> 31 for i in v):
+        raise W4A8Error(f"{[i for i in v if i >> 31]}: integers from 0 to 2^31 - 1 are expected")
+
+
 def padded_k(K: int, group: int = 128) -> int:
     """K rounded up to a whole number of 128-wide planes and of groups (the layout's
     row length)."""
@@ -265,6 +271,8 @@ def w4a8_route_experts(logits: torch.Tensor, k: int, ids: torch.Tensor, w: torch
     logits: bf16, fp16 or float32 [T][E]; ids: int32 [T][k] and w: float32 [T][k] (written);
     flags: W4A8_ROUTE_* OR-ed; bias: float32 [E] or None."""
     dev = _device_of_call(logits, "logits")
+    if (flags | n_group | topk_group) >> 31:
+        _need_c_ints(flags, n_group, topk_group)
     dtype = logits.dtype
     if dtype not in _LOGITS_TYPE:
         raise W4A8Error(f"logits must be bf16, fp16 or float32, got {dtype}")
@@ -487,7 +495,7 @@ _OUT_TYPE = {torch.float32: W8A8_F32, torch.bfloat16: W8A8_BF16, torch.float16: 
 
 
 def w8a8_packed_bytes(E: int, N: int, K: int, layout: int) -> int:
-    return lib().w8a8_packed_bytes(E, N, K, layout)
+    return 0 if any(i >> 31 for i in (E, N, K, layout)) else lib().w8a8_packed_bytes(E, N, K, layout)
 
 
 def w8a8_pack_weights(w: torch.Tensor, layout: int, packed: torch.Tensor, codes=None, scale=None):
@@ -498,6 +506,7 @@ def w8a8_pack_weights(w: torch.Tensor, layout: int, packed: torch.Tensor, codes=
         w = w.unsqueeze(0)
     _need(w.dim() == 3, "w must be [E][N][K]")
     E, N, K = w.shape
+    _need_c_ints(E, N, K, layout)
     _dev(packed, torch.uint8, "packed")
     if codes is not None:
         _dev(codes, torch.int8, "codes")
@@ -515,7 +524,7 @@ def _w8_packed_size(E: int, tiles: int, K: int) -> int:
 
 
 def w8a8_gemm_workspace_bytes(M, N, K) -> int:
-    return lib().w8a8_gemm_workspace_bytes(M, N, K)
+    return 0 if any(i >> 31 for i in (M, N, K)) else lib().w8a8_gemm_workspace_bytes(M, N, K)
 
 
 def w8a8_gemm(qa, sa, packed, N, K, y, ws, bias=None):
@@ -560,13 +569,15 @@ def w8a8_gemm_last_error(ws) -> int:
 
 
 def w8a8_moe_workspace_bytes(T, E, k, H, F) -> int:
-    return lib().w8a8_moe_workspace_bytes(T, E, k, H, F)
+    return 0 if any(i >> 31 for i in (T, E, k, H, F)) else lib().w8a8_moe_workspace_bytes(T, E, k, H, F)
 
 
 def w8a8_moe_forward(packed_up, packed_down, E, H, F, x, ids, w, out, ws):
     """The MoE expert FFN with W8A8 experts: the arguments of w4a8_moe_forward, weights from
     w8a8_pack_weights, ws sized by w8a8_moe_workspace_bytes."""
     dev = _device_of_call(x, "x")
+    if (E | F) >> 31:
+        _need_c_ints(E, F)
     if ids.dim() != 2:
         raise W4A8Error("ids must be [T][k]")
     T, k = ids.shape
