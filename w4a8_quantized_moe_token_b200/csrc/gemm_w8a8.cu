@@ -25,7 +25,7 @@
 // 128-wide K planes; two accumulators, so that a tile's epilogue overlaps the next tile's K
 // loop.  Every wait is bounded.
 //
-// Measured on B200.  16384 x 7168 -> 4096 (bf16 out): 286 us alone (3367 TOPS), 330-338 us
+// Measured on B200.  16384 x 7168 -> 4096 (bf16 out): 285 us alone (3375 TOPS), 330-346 us
 // repeated without a pause, when the power limit lowers the clock (tensor pipe 88 % active:
 // bound by it, and by power).  64 tokens, 6 of 64 experts, H 4096, F 1408: up 117 us, 97 % of
 // the measured copy rate, down 64 us, 88 % (bound by HBM).  One row, 2048 -> 7168: 6.0 us in a
@@ -269,7 +269,7 @@ __device__ __forceinline__ uint16_t to_bits16(float v) {
 }
 
 // predicated stores: a branch around each would keep the values' arithmetic from overlapping
-// (SwiGLU tiles of 16 K planes 41 against 37 us)
+// (SwiGLU tiles of 16 K planes 55.8 against 43.5 us)
 __device__ __forceinline__ void st_if(bool p, void* at, uint32_t v) {
     asm volatile("{\n\t.reg .pred p;\n\tsetp.ne.b32 p, %2, 0;\n\t@p st.global.b32 [%0], %1;\n\t}" ::"l"(at), "r"(v), "r"((int)p)
                  : "memory");

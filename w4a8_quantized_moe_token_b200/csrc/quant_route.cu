@@ -1278,7 +1278,7 @@ cudaError_t launch_act_scatter(const uint16_t* x, int T, int H, int Kp, int k, c
 cudaError_t launch_w8_act_scatter(const uint16_t* x, int T, int H, int Kp, int k, const int* inv, int rb, int8_t* act, float* s,
                                   cudaStream_t stream) {
     if (T == 0) return cudaSuccess;
-    // 3000 tokens of 1024 values to 4 places each: 14 us with a warp per token, 20 us with a CTA
+    // 3000 tokens of 1024 values to 4 places each: 12.7 us with a warp per token, 16 us with a CTA
     if (H <= 1024)
         return launch_pdl(H <= 512 ? act_scatter_short_kernel<1> : act_scatter_short_kernel<2>, ceil_div(T, 8), 256, 0, stream, x,
                           T, H, Kp, k, inv, rb, act, s);
@@ -1303,10 +1303,10 @@ cudaError_t launch_w8_requant(const uint16_t* h, int ldh, int F, int Kp, const i
                               int rows_cap, int rb, int8_t* act, float* s, cudaStream_t stream) {
     if (rows_cap == 0) return cudaSuccess;
     // A warp per row up to F = 2048, unless a CTA per row fits the GPU at once and a row keeps
-    // most of a CTA busy (F > 1024). CTA against warp at F = 1408: 384 rows 8.7 against 10.7 us,
-    // 1536 rows 10.7 both, 3840 rows 14.6 against 12.8, 49152 rows (F = 1536) 140 against 84; at
-    // F = 2048: 1920 rows 11.1 against 12.9, 3840 rows 14.8 against 14.7; at F = 1024, 160 rows
-    // of 512 experts 10.8 against 8.8.
+    // most of a CTA busy (F > 1024). CTA against warp at F = 1408: 384 rows 8.7 against 10.5 us,
+    // 1536 rows 10.7 and 10.8, 3840 rows 14.7 and 12.7, 49152 rows (F = 1536) 104.7 and 60.9; at
+    // F = 2048: 1920 rows 11.5 and 12.3, 3840 rows 16.4 and 14.8; at F = 1024, 160 rows of 512
+    // experts 8.7 both.
     if (F <= 2048 && (F <= 1024 || rows_cap > 16 * sm_count()))
         return launch_pdl(F <= 512    ? requant_short_kernel<1>
                           : F <= 1024 ? requant_short_kernel<2>

@@ -17,8 +17,10 @@
 // a bias the keys are the logits themselves and nothing is ever in doubt.
 //
 // Bound by instruction issue, not by memory: 16384 x 384 fp32 logits (sigmoid, bias, 4 of 8
-// groups) take 31-33 us on B200, 1477 warp instructions per token, for 4 us of bytes; one
-// token 4.8 us, 64 x 64 (softmax) 3.4 us, both in a graph.
+// groups) take 32-34 us on B200, 1482 warp instructions per token, for 4 us of bytes; one
+// token 4.9 us, 64 x 64 (softmax) 3.2 us, both in a graph.  (At 40 registers the rare 64-bit
+// functions, called out of line, cost every instance a stack frame of 104 to 128 bytes and some
+// spills: 44 bytes stored and 100 loaded with 384 experts.)
 #include <math_constants.h>
 
 #include <type_traits>
