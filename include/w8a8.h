@@ -78,8 +78,8 @@ int w8a8_gemm_last_error(const void* ws, void* stream);
  * quantisation and combine of w4a8_moe_forward,
  *   out[t] = sum_j w[t][j] * Down_e(SwiGLU(Up_e(x[t]))),  e = ids[t][j],
  * h = silu(gate) * up (fp32, within 7 roundings) rounded to bf16 and requantised per token
- * before Down, the experts' outputs summed in fp32, j ascending, and rounded once to bf16.  An id out of range drops
- * its slot and sets bit 1 of the error word.
+ * before Down, the experts' outputs summed in fp32, j ascending, and rounded once to bf16.
+ * An id out of range drops its slot and sets bit 1 of the error word.
  *   packed_up   : from w8a8_pack_weights(E, 2F, H, W4A8_LAYOUT_GATEUP).
  *   packed_down : from w8a8_pack_weights(E, H, F, W4A8_LAYOUT_PLAIN).
  * The workspace is laid out as w4a8_moe_forward's, its stages readable with w4a8_debug_dump
